@@ -15,10 +15,15 @@
 #include <utility>
 
 #include "dispatch.h"
+#include "host_util.h"
 
 namespace {
 
 thread_local std::string g_last_error;
+
+}  // namespace
+
+namespace gqa {
 
 gqa_status fail(gqa_status s, const char* fmt, ...) {
   char buf[512];
@@ -57,6 +62,16 @@ int current_sm_count(gqa_status* st) {
   if (dev >= 0 && dev < 128) cache[dev] = n;
   return n;
 }
+
+}  // namespace gqa
+
+namespace {
+
+using gqa::aligned16;
+using gqa::check_shape;
+using gqa::cuda_fail;
+using gqa::current_sm_count;
+using gqa::fail;
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static std::once_flag once;
@@ -106,11 +121,17 @@ constexpr long long kTqMinSplitBytes = 32 << 10;
 // The TurboQuant row kernel: 8 warps and ~94 KB of shared memory, one CTA per SM.
 constexpr int kTqRowsCtasPerSm = 1;
 
+}  // namespace
+
+namespace gqa {
+
+void set_last_error(const char* msg) { g_last_error = msg; }
+
 // Shapes that do not depend on the device.
 gqa_status check_shape(int n_tok, int n_heads, int n_kv_heads, int head_dim, int max_kv_len,
                        int kind) {
-  if (kind != GQA_KIND_F16 && kind != GQA_KIND_Q8 && kind != GQA_KIND_TQ)
-    return fail(GQA_EINVAL, "kind must be 0, 1 or 2");
+  if (kind < GQA_KIND_F16 || kind > GQA_KIND_F16_WINDOW)
+    return fail(GQA_EINVAL, "kind must be 0 .. 4");
   if (n_tok < 0 || n_tok > 65535) return fail(GQA_EINVAL, "n_tok %d outside [0, 65535]", n_tok);
   if (n_heads <= 0 || n_kv_heads <= 0 || n_kv_heads > 65535)
     return fail(GQA_EINVAL, "n_heads %d / n_kv_heads %d", n_heads, n_kv_heads);
@@ -125,12 +146,6 @@ gqa_status check_shape(int n_tok, int n_heads, int n_kv_heads, int head_dim, int
     return fail(GQA_EUNSUPPORTED, "group size %d > 16", n_heads / n_kv_heads);
   return GQA_OK;
 }
-
-}  // namespace
-
-namespace gqa {
-
-void set_last_error(const char* msg) { g_last_error = msg; }
 
 // CUDA-core kernel: heads per warp for the query heads one CTA serves (at most 4 after the
 // head split), four row slices per stage.
@@ -255,6 +270,9 @@ gqa_status attn_decode_plan(int n_tok, int n_seq, int n_heads, int n_kv_heads, i
   if (st != GQA_OK) return st;
   if (n_seq <= 0) return fail(GQA_EINVAL, "n_seq %d must be > 0", n_seq);
   plan->row_group = 1;
+  if (kind == GQA_KIND_Q4 || kind == GQA_KIND_F16_WINDOW)
+    return gqa::plan_visible(n_tok, n_seq, n_heads, n_kv_heads, head_dim, max_kv_len, budget, kind,
+                             num_sms, plan);
   if (kind == GQA_KIND_F16) budget = -1;
   if (budget == 0 || budget < -1) return fail(GQA_EINVAL, "budget %d (use -1 for dense)", budget);
   if (num_sms <= 0) {

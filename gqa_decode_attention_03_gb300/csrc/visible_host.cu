@@ -1,0 +1,140 @@
+// visible_host.cu -- attn_decode_q4 and attn_decode_f16_window: argument checks, the plan of their
+// split, and the launch.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+#include "host_util.h"
+#include "visible_dispatch.h"
+
+namespace gqa {
+
+bool q4_scale_ok(float s);  // append_q4.cu
+
+gqa_status plan_visible(int n_tok, int n_seq, int n_heads, int n_kv_heads, int head_dim,
+                        int max_kv_len, int budget, int kind, int num_sms, gqa_plan* plan) {
+  (void)n_seq, (void)head_dim, (void)n_kv_heads, (void)num_sms, (void)kind;
+  if (budget == 0 || budget < -1)
+    return fail(GQA_EINVAL, "budget %d: window + n_sink, or -1 for every position", budget);
+  const int n = budget > 0 ? std::min(max_kv_len, budget) : max_kv_len;
+  plan->chunk = std::max(n, 1);
+  plan->n_split = 1;
+  plan->tile = 1;
+  plan->grid_x = n_heads;
+  plan->grid_y = n_tok;
+  plan->grid_z = 1;
+  return GQA_OK;
+}
+
+static gqa_status visible_common(int kind, const float* q, const void* kc, const void* vc,
+                                 const uint8_t* ksc, const uint8_t* vsc, float k_scale,
+                                 float v_scale, int window, int n_sink, float* out,
+                                 const int32_t* kv_len, const int32_t* seq_of, int n_tok,
+                                 int n_seq, int n_heads, int n_kv_heads, int head_dim,
+                                 int64_t cache_cap, int max_kv_len, float scale,
+                                 const float* gate, int64_t gate_stride, void* ws,
+                                 size_t ws_bytes, int32_t* err_word, cudaStream_t stream) {
+  const bool q4 = kind == GQA_KIND_Q4;
+  gqa_status st = check_shape(n_tok, n_heads, n_kv_heads, head_dim, max_kv_len, kind);
+  if (st != GQA_OK) return st;
+  if (n_sink < 0 || window < 0 || (!q4 && window == 0))
+    return fail(GQA_EINVAL, "window %d, n_sink %d", window, n_sink);
+  if (n_seq <= 0 || cache_cap <= 0) return fail(GQA_EINVAL, "n_seq and cache_cap must be > 0");
+  if (n_tok == 0) return GQA_OK;
+  if (!q || !kc || !vc || !out || !kv_len) return fail(GQA_EINVAL, "a required pointer is NULL");
+  if (!aligned16(q) || !aligned16(out) || !aligned16(kc) || !aligned16(vc))
+    return fail(GQA_EINVAL, "q, out and the caches must be 16-byte aligned");
+  if (q4) {
+    if (!ksc || !vsc) return fail(GQA_EINVAL, "scale pointer is NULL");
+    if (!aligned16(ksc) || !aligned16(vsc))
+      return fail(GQA_EINVAL, "scales must be 16-byte aligned");
+    if (cache_cap % 16) return fail(GQA_EINVAL, "cache_cap must be a multiple of 16");
+    if (!q4_scale_ok(k_scale) || !q4_scale_ok(v_scale))
+      return fail(GQA_EINVAL, "k_scale and v_scale must be powers of two in [2^-64, 2^64]");
+  }
+  if (gate && (gate_stride < head_dim || (reinterpret_cast<uintptr_t>(gate) & 3)))
+    return fail(GQA_EINVAL, "gate must be 4-byte aligned with gate_stride >= head_dim");
+  if ((reinterpret_cast<uintptr_t>(kv_len) | reinterpret_cast<uintptr_t>(seq_of) |
+       reinterpret_cast<uintptr_t>(err_word)) & 3)
+    return fail(GQA_EINVAL, "kv_len, seq_of and err_word must be 4-byte aligned");
+  if ((int64_t)n_seq * cache_cap > INT32_MAX)
+    return fail(GQA_EUNSUPPORTED, "n_seq * cache_cap must stay below 2^31 rows");
+  if (!seq_of && n_seq < n_tok) return fail(GQA_EINVAL, "seq_of NULL needs n_seq >= n_tok");
+  if (!std::isfinite(scale)) return fail(GQA_EINVAL, "scale is not finite");
+  const int max_len = (int)std::min<int64_t>(max_kv_len, cache_cap);
+  const int budget = window ? (int)std::min<int64_t>((int64_t)window + n_sink, INT_MAX) : -1;
+  gqa_plan plan;
+  st = attn_decode_plan(n_tok, n_seq, n_heads, n_kv_heads, head_dim, max_len, budget, kind, 0,
+                        &plan);
+  if (st != GQA_OK) return st;
+  if (plan.merge && (!ws || ws_bytes < plan.ws_bytes || !aligned16(ws)))
+    return fail(GQA_EWORKSPACE, "workspace needs %zu bytes (16-byte aligned), got %zu",
+                plan.ws_bytes, ws ? ws_bytes : (size_t)0);
+
+  VisibleParams vp{};
+  PartialParams& p = vp.base;
+  p.q = q;
+  p.kc = kc;
+  p.vc = vc;
+  p.ksc = reinterpret_cast<const __half*>(ksc);
+  p.vsc = reinterpret_cast<const __half*>(vsc);
+  p.kv_len = kv_len;
+  p.seq_of = seq_of;
+  p.out = out;
+  p.err = err_word;
+  p.n_tok = n_tok;
+  p.n_seq = n_seq;
+  p.n_heads = n_heads;
+  p.n_kv_heads = n_kv_heads;
+  p.group = n_heads / n_kv_heads;
+  p.cache_cap = cache_cap;
+  p.max_kv_len = max_len;
+  p.chunk = plan.chunk;
+  p.n_split = plan.n_split;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.merge = plan.merge;
+  p.gate = gate;
+  p.gate_stride = gate ? gate_stride : 0;
+  vp.window = window;
+  vp.n_sink = n_sink;
+  vp.k_scale = k_scale;
+  vp.v_scale = v_scale;
+  const cudaError_t e = q4 ? launch_q4(head_dim, vp, plan, stream)
+                           : launch_f16_window(head_dim, vp, plan, stream);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return cuda_fail(e, q4 ? "attn_decode_q4 launch" : "attn_decode_f16_window launch");
+  }
+  return GQA_OK;
+}
+
+}  // namespace gqa
+
+extern "C" gqa_status attn_decode_q4(const float* q, const uint8_t* kq, const uint8_t* vq,
+                                     const uint8_t* ksc, const uint8_t* vsc, float k_scale,
+                                     float v_scale, int window, int n_sink, float* out,
+                                     const int32_t* kv_len, const int32_t* seq_of, int n_tok,
+                                     int n_seq, int n_heads, int n_kv_heads, int head_dim,
+                                     int64_t cache_cap, int max_kv_len, float scale,
+                                     const float* gate, int64_t gate_stride, void* ws,
+                                     size_t ws_bytes, int32_t* err_word, cudaStream_t stream) {
+  return gqa::visible_common(GQA_KIND_Q4, q, kq, vq, ksc, vsc, k_scale, v_scale, window,
+                             window ? n_sink : 0, out, kv_len, seq_of, n_tok, n_seq, n_heads,
+                             n_kv_heads, head_dim, cache_cap, max_kv_len, scale, gate, gate_stride,
+                             ws, ws_bytes, err_word, stream);
+}
+
+extern "C" gqa_status attn_decode_f16_window(const float* q, const uint16_t* k_cache,
+                                             const uint16_t* v_cache, int window, int n_sink,
+                                             float* out, const int32_t* kv_len,
+                                             const int32_t* seq_of, int n_tok, int n_seq,
+                                             int n_heads, int n_kv_heads, int head_dim,
+                                             int64_t cache_cap, int max_kv_len, float scale,
+                                             const float* gate, int64_t gate_stride, void* ws,
+                                             size_t ws_bytes, int32_t* err_word,
+                                             cudaStream_t stream) {
+  return gqa::visible_common(GQA_KIND_F16_WINDOW, q, k_cache, v_cache, nullptr, nullptr, 1.f, 1.f,
+                             window, n_sink, out, kv_len, seq_of, n_tok, n_seq, n_heads,
+                             n_kv_heads, head_dim, cache_cap, max_kv_len, scale, gate, gate_stride,
+                             ws, ws_bytes, err_word, stream);
+}

@@ -17,7 +17,7 @@ import torch
 _LIB_PATH = Path(__file__).resolve().parent / "lib" / "libgqadecode.so"
 
 GQA_OK, GQA_EINVAL, GQA_EWORKSPACE, GQA_EUNSUPPORTED, GQA_ECUDA = range(5)
-KIND_F16, KIND_Q8, KIND_TQ = 0, 1, 2
+KIND_F16, KIND_Q8, KIND_TQ, KIND_Q4, KIND_F16_WINDOW = 0, 1, 2, 3, 4
 ERR_KVLEN_RANGE, ERR_ID_RANGE, ERR_SEQ_RANGE, ERR_TIMEOUT = 0x1, 0x2, 0x4, 0x8
 
 # Every symbol the header declares (checked by the CPU test suite).
@@ -25,7 +25,8 @@ EXPORTS = ("attn_decode_plan", "attn_decode_workspace_bytes", "attn_decode_f16",
            "attn_decode_q8_sel", "attn_merge", "gqa_status_string", "gqa_last_error",
            "gqa_abi_version", "attn_decode_f16_noalloc", "attn_select_topk", "kv_append_q8", "attn_merge_gated",
            "attn_decode_tq", "attn_decode_q8_sel_sg", "kv_append_q8_sg", "attn_decode_f16_gated",
-           "attn_decode_q8_sel_gated", "attn_decode_tq_gated")
+           "attn_decode_q8_sel_gated", "attn_decode_tq_gated", "kv_append_q4", "kv_read_q4",
+           "attn_decode_q4", "attn_decode_f16_window")
 NOALLOC_SCRATCH_BYTES = 16 << 20  # GQA_NOALLOC_SCRATCH_BYTES in include/gqa_decode.h
 
 
@@ -82,6 +83,16 @@ def _load():
     lib.attn_decode_tq_gated.argtypes = [P, P, P, P, P, P, P, ctypes.POINTER(F), P, F, F, P, P, P,
                                          I, I, I, I, I, I64, I, P, I64, P, SZ, P, P]
     lib.attn_decode_tq_gated.restype = I
+    lib.kv_append_q4.argtypes = [P, P, I, I, I, P, P, F, F, P, P, P, P, I, I64, P, P]
+    lib.kv_append_q4.restype = I
+    lib.kv_read_q4.argtypes = [P, P, P, P, I, I64, I, I, I, P, P, F, F, P, P, I, P, P]
+    lib.kv_read_q4.restype = I
+    lib.attn_decode_q4.argtypes = [P, P, P, P, P, F, F, I, I, P, P, P, I, I, I, I, I, I64, I, F, P,
+                                   I64, P, SZ, P, P]
+    lib.attn_decode_q4.restype = I
+    lib.attn_decode_f16_window.argtypes = [P, P, P, I, I, P, P, P, I, I, I, I, I, I64, I, F, P,
+                                           I64, P, SZ, P, P]
+    lib.attn_decode_f16_window.restype = I
     lib.attn_merge.argtypes = [P, P, I, I, I, I, P, P]
     lib.attn_merge.restype = I
     lib.gqa_status_string.argtypes = [I]
@@ -108,6 +119,10 @@ def _ptr(x):
 # the current stream's raw handle without building a torch Stream object (several us a call)
 _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _GET_DEVICE = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _current_device():
+    return _GET_DEVICE() if _GET_DEVICE is not None else torch.cuda.current_device()
 
 
 def _stream(stream):
@@ -375,6 +390,173 @@ def kv_append_q8(k_new, v_new, kq, vq, ksc, vsc, seq, t0, stream=None):
     _check(LIB.kv_append_q8_sg(_ptr(k_new), _ptr(v_new), n_new, Hk, D, D // ksc.shape[3],
                                _ptr(kq), _ptr(vq), _ptr(ksc), _ptr(vsc), n_seq, cap, int(seq),
                                int(t0), _stream(stream)))
+
+
+def _need_all(device, *specs):
+    """``_need`` over (tensor, dtype, name, ndim), and all on the current CUDA device."""
+    for x, dtype, name, ndim in specs:
+        _need(x, dtype, name, ndim)
+        if x.get_device() != device:
+            raise ValueError(f"{name} is on cuda:{x.get_device()}, the current device is "
+                             f"cuda:{device}")
+
+
+def _need_err(err, device):
+    if err is not None:
+        _need_all(device, (err, torch.int32, "err", None))
+        if err.numel() < 1:
+            raise ValueError("err must hold one int32")
+
+
+def _q4_cache(kq, vq, ksc, vsc, device):
+    """(n_seq, Hk, cap, D) of a 4-bit cache, checked."""
+    _need_all(device, (kq, torch.uint8, "kq", 4), (vq, torch.uint8, "vq", 4),
+              (ksc, torch.uint8, "ksc", 4), (vsc, torch.uint8, "vsc", 4))
+    n_seq, Hk, cap, D2 = kq.shape
+    if vq.shape != kq.shape or vsc.shape != ksc.shape or ksc.shape != (n_seq, Hk, cap, D2 // 8):
+        raise ValueError("shape mismatch between the 4-bit cache's codes and scales")
+    return n_seq, Hk, cap, 2 * D2
+
+
+def _ragged(row_off, t0, n_seq, device):
+    _need_all(device, (row_off, torch.int32, "row_off", 1), (t0, torch.int32, "t0", 1))
+    if row_off.numel() != n_seq + 1 or t0.numel() != n_seq:
+        raise ValueError("row_off must hold n_seq + 1 entries and t0 n_seq")
+
+
+def kv_append_q4(k_new, v_new, kq, vq, ksc, vsc, row_off, t0, k_scale=1.0, v_scale=1.0, err=None,
+                 stream=None):
+    """Quantise fp32 rows k_new / v_new [n_rows][Hk][D] of a ragged batch into the 4-bit cache.
+
+    kq, vq [n_seq][Hk][cap][D/2] uint8 (two e2m1 codes a byte, the even dim low); ksc, vsc
+    [n_seq][Hk][cap][D/16] uint8 (e4m3 bits, one per 16 dims); cap a multiple of 16.  Sequence s
+    takes rows row_off[s] .. row_off[s+1]-1 (row_off [n_seq+1] int32) at positions t0[s] ..
+    (t0 [n_seq] int32); rows from row_off[n_seq] on are left out.  k_scale, v_scale: powers of two
+    that the values are divided by first.
+    """
+    device = _current_device()
+    n_seq, Hk, cap, D = _q4_cache(kq, vq, ksc, vsc, device)
+    _need_all(device, (k_new, torch.float32, "k_new", 3), (v_new, torch.float32, "v_new", 3))
+    _ragged(row_off, t0, n_seq, device)
+    _need_err(err, device)
+    n = k_new.shape[0]
+    if k_new.shape != (n, Hk, D) or v_new.shape != (n, Hk, D):
+        raise ValueError("shape mismatch between new rows and the cache")
+    _check(LIB.kv_append_q4(_ptr(k_new), _ptr(v_new), n, Hk, D, _ptr(row_off), _ptr(t0),
+                            float(k_scale), float(v_scale), _ptr(kq), _ptr(vq), _ptr(ksc),
+                            _ptr(vsc), n_seq, cap, _ptr(err), _stream(stream)))
+
+
+def kv_read_q4(kq, vq, ksc, vsc, row_off, t0, k_out=None, v_out=None, n_rows=None, k_scale=1.0,
+               v_scale=1.0, dtype=torch.float32, err=None, stream=None):
+    """The values of rows of the 4-bit cache: (k, v) [n_rows][Hk][D] in fp32 or fp16, the rows
+    addressed as in ``kv_append_q4``.  Give k_out and v_out, or n_rows (and dtype) for new ones."""
+    device = _current_device()
+    n_seq, Hk, cap, D = _q4_cache(kq, vq, ksc, vsc, device)
+    _ragged(row_off, t0, n_seq, device)
+    _need_err(err, device)
+    if (k_out is None) != (v_out is None):
+        raise ValueError("give both k_out and v_out, or neither")
+    if k_out is None:
+        if n_rows is None:
+            raise ValueError("give k_out and v_out, or n_rows")
+        k_out = torch.zeros((int(n_rows), Hk, D), dtype=dtype, device=kq.device)
+        v_out = torch.zeros_like(k_out)
+    elif not isinstance(k_out, torch.Tensor):
+        raise TypeError("k_out must be a torch.Tensor")
+    else:
+        dtype = k_out.dtype
+    if dtype not in (torch.float32, torch.float16):
+        raise TypeError(f"rows are read as float32 or float16, not {dtype}")
+    _need_all(device, (k_out, dtype, "k_out", 3), (v_out, dtype, "v_out", 3))
+    n = k_out.shape[0]
+    if k_out.shape != (n, Hk, D) or v_out.shape != (n, Hk, D) or n_rows not in (None, n):
+        raise ValueError("shape mismatch between the output rows and the cache")
+    _check(LIB.kv_read_q4(_ptr(kq), _ptr(vq), _ptr(ksc), _ptr(vsc), n_seq, cap, n, Hk, D,
+                          _ptr(row_off), _ptr(t0), float(k_scale), float(v_scale), _ptr(k_out),
+                          _ptr(v_out), 1 if dtype == torch.float16 else 0, _ptr(err),
+                          _stream(stream)))
+    return k_out, v_out
+
+
+def _visible_args(q, kv_len, seq_of, n_seq, Hk, cap, Dk, scale, max_kv_len, window, n_sink, out,
+                  ws, err, gate, gate_stride, kind, device):
+    """The arguments that the calls with a visible set share, checked: (T, H, D, scale,
+    max_kv_len, window, n_sink, out, ws, gate_stride)."""
+    _need_all(device, (q, torch.float32, "q", 3), (kv_len, torch.int32, "kv_len", 1))
+    if seq_of is not None:
+        _need_all(device, (seq_of, torch.int32, "seq_of", 1))
+    T, H, D = q.shape
+    if Dk != D or kv_len.numel() != T or (seq_of is not None and seq_of.numel() != T):
+        raise ValueError("shape mismatch between q, caches, kv_len and seq_of")
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    max_kv_len = cap if max_kv_len is None else int(max_kv_len)
+    window, n_sink = int(window or 0), int(n_sink)
+    if not (0 <= window < 1 << 31 and 0 <= n_sink < 1 << 31 and max_kv_len < 1 << 31):
+        raise ValueError("window, n_sink and max_kv_len must lie in [0, 2^31)")
+    if out is None:
+        out = torch.empty_like(q)
+    _need_all(device, (out, torch.float32, "out", 3))
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if T and out.data_ptr() == q.data_ptr():
+        raise ValueError("out must not be q")
+    if ws is None:
+        budget = min(window + n_sink, (1 << 31) - 1) if window else -1
+        ws = alloc_workspace(T, H, Hk, D, min(max_kv_len, cap), budget, kind, q.device, n_seq)
+    elif not (ws.is_cuda and ws.is_contiguous() and ws.get_device() == device):
+        raise ValueError("ws must be a contiguous tensor on the current CUDA device")
+    _need_err(err, device)
+    gs = 0
+    if gate is not None:
+        gs = _gate_args(gate, gate_stride, T, H, D)
+        _need_all(device, (gate, torch.float32, "gate", None))
+    return T, H, D, scale, max_kv_len, window, n_sink, out, ws, gs
+
+
+def attn_decode_q4(q, kq, vq, ksc, vsc, kv_len, scale=None, k_scale=1.0, v_scale=1.0, window=None,
+                   n_sink=0, seq_of=None, max_kv_len=None, out=None, ws=None, err=None,
+                   stream=None, gate=None, gate_stride=None):
+    """Decode attention over a 4-bit cache (``kv_append_q4``'s); returns ``out [T][H][D]`` fp32.
+
+    q [T][H][D] fp32; kv_len [T] int32 (device); seq_of [T] int32 or None.  window: row t sees
+    only its last `window` positions and the first n_sink (None: every position).  gate: optional
+    fp32 sigmoid output gate, see ``_gate_args``.
+    """
+    device = _current_device()
+    n_seq, Hk, cap, Dk = _q4_cache(kq, vq, ksc, vsc, device)
+    T, H, D, scale, max_kv_len, window, n_sink, out, ws, gs = _visible_args(
+        q, kv_len, seq_of, n_seq, Hk, cap, Dk, scale, max_kv_len, window,
+        n_sink if window else 0, out, ws, err, gate, gate_stride, KIND_Q4, device)
+    _check(LIB.attn_decode_q4(_ptr(q), _ptr(kq), _ptr(vq), _ptr(ksc), _ptr(vsc), float(k_scale),
+                              float(v_scale), window, n_sink, _ptr(out), _ptr(kv_len),
+                              _ptr(seq_of), T, n_seq, H, Hk, D, cap, max_kv_len, scale, _ptr(gate),
+                              gs, _ptr(ws), ws.numel() * ws.element_size(), _ptr(err),
+                              _stream(stream)))
+    return out
+
+
+def attn_decode_f16_window(q, k_cache, v_cache, kv_len, window, n_sink=0, scale=None, seq_of=None,
+                           max_kv_len=None, out=None, ws=None, err=None, stream=None, gate=None,
+                           gate_stride=None):
+    """``attn_decode_f16`` through a sliding window: row t sees its last `window` positions and the
+    first n_sink.  Rows that share a sequence (a prefill chunk) each have their own window."""
+    device = _current_device()
+    _need_all(device, (k_cache, torch.float16, "k_cache", 4),
+              (v_cache, torch.float16, "v_cache", 4))
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache shapes differ")
+    if not window or int(window) < 1:
+        raise ValueError("window must be >= 1")
+    n_seq, cap, Hk, Dk = k_cache.shape
+    T, H, D, scale, max_kv_len, window, n_sink, out, ws, gs = _visible_args(
+        q, kv_len, seq_of, n_seq, Hk, cap, Dk, scale, max_kv_len, window, n_sink, out, ws, err,
+        gate, gate_stride, KIND_F16_WINDOW, device)
+    _check(LIB.attn_decode_f16_window(_ptr(q), _ptr(k_cache), _ptr(v_cache), window, n_sink,
+                                      _ptr(out), _ptr(kv_len), _ptr(seq_of), T, n_seq, H, Hk, D,
+                                      cap, max_kv_len, scale, _ptr(gate), gs, _ptr(ws),
+                                      ws.numel() * ws.element_size(), _ptr(err), _stream(stream)))
+    return out
 
 
 def attn_merge(part, n_valid, out=None, gate=None, gate_stride=None, stream=None):

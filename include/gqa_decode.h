@@ -71,6 +71,8 @@ typedef enum gqa_status {
 #define GQA_KIND_F16 0
 #define GQA_KIND_Q8 1
 #define GQA_KIND_TQ 2 /* TurboQuant-compressed caches (attn_decode_tq) */
+#define GQA_KIND_Q4 3 /* 4-bit caches (attn_decode_q4) */
+#define GQA_KIND_F16_WINDOW 4 /* f16 caches seen through a window (attn_decode_f16_window) */
 
 /* The split plan the decode calls use (exposed so hosts and tests can inspect it). */
 typedef struct gqa_plan {
@@ -365,6 +367,88 @@ gqa_status attn_decode_tq_gated(const float* q_rot, const float* q_jl, const uin
                                 int n_kv_heads, int head_dim, int64_t cache_cap, int max_kv_len,
                                 const float* gate, int64_t gate_stride, void* ws,
                                 size_t ws_bytes, int32_t* err_word, cudaStream_t stream);
+
+/*
+ * A 4-bit K/V cache.  A row of head_dim values is stored as e2m1 codes, one e4m3 scale per 16
+ * dims, and a scale of the whole cache:
+ *   value = e2m1(code) * e4m3(scale) * k_scale     (v_scale for V; exact in fp32)
+ * e2m1: bit 3 the sign, bits 0-2 one of {0, 0.5, 1, 1.5, 2, 3, 4, 6}.  e4m3: the sign bit is not
+ * used and has to be 0; 0x7f is not used.
+ *   kq, vq        device uint8 [n_seq][n_kv_heads][cache_cap][head_dim/2], 16-byte aligned; dim 2i
+ *                 in the low nibble of byte i, dim 2i + 1 in the high one
+ *   ksc, vsc      device uint8 [n_seq][n_kv_heads][cache_cap][head_dim/16], 16-byte aligned
+ *   cache_cap     a multiple of 16, so that 16 positions of a KV head start on 16 bytes
+ *   k_scale, v_scale  powers of two in [2^-64, 2^64]: multiplying by one rounds nothing.  e4m3
+ *                 covers 18 binades, so the pair only has to bring the cache's values near 1.
+ *   head_dim in {64, 128, 256}
+ * The calls below read and write rows of a ragged batch: row r of the batch belongs to the
+ * sequence s with row_off[s] <= r < row_off[s + 1] and stands for position t0[s] + r - row_off[s].
+ *   row_off       device int32 [n_seq + 1], ascending from 0; row_off[n_seq] <= n_rows.  A sequence
+ *                 may have no rows; rows from row_off[n_seq] on (a padded batch) are left alone.
+ *   t0            device int32 [n_seq]
+ * No two rows name the same position.  A row whose position falls outside [0, cache_cap) is
+ * skipped and flagged GQA_ERR_KVLEN_RANGE; a row that no sequence holds, in a row_off that does
+ * not ascend from 0, is skipped and flagged GQA_ERR_SEQ_RANGE.
+ *
+ * kv_append_q4 -- quantise new fp32 rows k_new, v_new [n_rows][n_kv_heads][head_dim] (16-byte
+ * aligned) into the cache.  For 16 dims y = x / k_scale: scale = e4m3 nearest to amax|y| / 6 (at
+ * most 448), code = e2m1 nearest to y / scale, ties to the even code in both; the quotients are
+ * not rounded first.  A scale of 0 gives codes 0; NaN counts as 0, values past the largest code
+ * take it.
+ */
+gqa_status kv_append_q4(const float* k_new, const float* v_new, int n_rows, int n_kv_heads,
+                        int head_dim, const int32_t* row_off, const int32_t* t0, float k_scale,
+                        float v_scale, uint8_t* kq, uint8_t* vq, uint8_t* ksc, uint8_t* vsc,
+                        int n_seq, int64_t cache_cap, int32_t* err_word, cudaStream_t stream);
+
+/*
+ * kv_read_q4 -- the values of cache rows, as fp32 (out_f16 0) or rounded to f16 (out_f16 1), into
+ * k_out, v_out [n_rows][n_kv_heads][head_dim] (16-byte aligned): with f16 the rows of one sequence
+ * are laid out as attn_decode_f16's cache holds them.  Other arguments as kv_append_q4.
+ */
+gqa_status kv_read_q4(const uint8_t* kq, const uint8_t* vq, const uint8_t* ksc,
+                      const uint8_t* vsc, int n_seq, int64_t cache_cap, int n_rows,
+                      int n_kv_heads, int head_dim, const int32_t* row_off, const int32_t* t0,
+                      float k_scale, float v_scale, void* k_out, void* v_out, int out_f16,
+                      int32_t* err_word, cudaStream_t stream);
+
+/*
+ * Attention through a sliding window with sinks: row t sees position j < kv_len[t] if
+ *   j >= kv_len[t] - window   (the last `window` positions), or
+ *   j < n_sink                (the first positions, which stay visible),
+ * each once.  window 0 means no window (every position; attn_decode_q4 only).  Nothing outside
+ * that set reaches the output.
+ *
+ * attn_decode_q4 -- decode attention over a 4-bit cache (layout above), dense or windowed.
+ *   window        >= 0; n_sink >= 0 (not used with window 0)
+ *   gate          sigmoid output gate as in the _gated calls above, or NULL
+ *   ws, ws_bytes  attn_decode_workspace_bytes(..., budget, GQA_KIND_Q4) with budget =
+ *                 window + n_sink, or -1 without a window; zeroed once like attn_decode_f16's
+ *   other arguments and errors as attn_decode_f16
+ */
+gqa_status attn_decode_q4(const float* q, const uint8_t* kq, const uint8_t* vq,
+                          const uint8_t* ksc, const uint8_t* vsc, float k_scale, float v_scale,
+                          int window, int n_sink, float* out, const int32_t* kv_len,
+                          const int32_t* seq_of, int n_tok, int n_seq, int n_heads,
+                          int n_kv_heads, int head_dim, int64_t cache_cap, int max_kv_len,
+                          float scale, const float* gate, int64_t gate_stride, void* ws,
+                          size_t ws_bytes, int32_t* err_word, cudaStream_t stream);
+
+/*
+ * attn_decode_f16_window -- attn_decode_f16 through a window with sinks.
+ *   window        >= 1; n_sink >= 0
+ *   gate          sigmoid output gate as in the _gated calls above, or NULL
+ *   ws, ws_bytes  attn_decode_workspace_bytes(..., window + n_sink, GQA_KIND_F16_WINDOW); zeroed
+ *                 once like attn_decode_f16's
+ *   other arguments and errors as attn_decode_f16
+ */
+gqa_status attn_decode_f16_window(const float* q, const uint16_t* k_cache,
+                                  const uint16_t* v_cache, int window, int n_sink, float* out,
+                                  const int32_t* kv_len, const int32_t* seq_of, int n_tok,
+                                  int n_seq, int n_heads, int n_kv_heads, int head_dim,
+                                  int64_t cache_cap, int max_kv_len, float scale,
+                                  const float* gate, int64_t gate_stride, void* ws,
+                                  size_t ws_bytes, int32_t* err_word, cudaStream_t stream);
 
 /* Human-readable name of a status; static storage. */
 const char* gqa_status_string(gqa_status s);

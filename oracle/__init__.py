@@ -14,15 +14,19 @@ pins must catch).  No function here is "parity unpinned".
 from .gqa_oracle import (  # noqa: F401
     attend_positions,
     decode_f16,
+    decode_f16_window,
+    decode_q4,
     decode_q8,
     decode_tq,
     hadamard,
     dequant_f16,
+    dequant_q4,
     dequant_q8,
     gated_merge,
     lse_merge,
     order_key,
     output_gate,
+    quantize_q4,
     quantize_q8,
     select_topk_cells,
     selected_positions,
@@ -30,4 +34,5 @@ from .gqa_oracle import (  # noqa: F401
     split_partials_q8,
     unpack_polar,
     unpack_signs,
+    visible_positions,
 )

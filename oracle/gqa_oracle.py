@@ -398,3 +398,85 @@ def decode_tq(q_rot, q_jl, k_polar, k_jl, k_norms, v_polar, v_norms, centroids, 
             acc = w @ (vnorm[:, None] * c[vidx])
             out[i, h] = sg * (Hd @ acc) / np.sqrt(D)
     return out
+
+
+# ----------------------------------------------------------------------------- 4-bit cache
+
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+E4M3 = np.array([c * 2.0 ** -9 if c < 8 else (8 + c % 8) * 2.0 ** (c // 8 - 10)
+                 for c in range(127)])  # codes 0 .. 126 (0 .. 448)
+Q4_GROUP = 16  # dims sharing an e4m3 scale
+
+
+def _nearest_code(x, grid) -> np.ndarray:
+    """Code of the grid value (per row of `grid`, or one grid) nearest to x >= 0, ties to the even
+    code, past the end the last: one comparison per midpoint, which float64 holds exactly."""
+    mid = (grid[..., 1:] + grid[..., :-1]) / 2
+    code = np.zeros(x.shape, dtype=np.int64)
+    for i in range(mid.shape[-1]):
+        code += (x > mid[..., i]) | ((x == mid[..., i]) & (i % 2 == 1))
+    return code
+
+
+def quantize_q4(x, scale: float = 1.0) -> tuple[np.ndarray, np.ndarray]:
+    """fp32 rows [..., D] -> (packed codes [..., D/2] uint8, scale bytes [..., D/16] uint8).
+    y = x / scale; per 16 dims the e4m3 value nearest to amax|y| / 6, then the e2m1 codes nearest
+    to y / that; ties to the even code; NaN counts as 0, a scale of 0 gives codes 0."""
+    y = np.asarray(x, dtype=np.float32).astype(np.float64) / scale
+    y = np.where(np.isnan(y), 0.0, y)
+    y = y.reshape(*y.shape[:-1], -1, Q4_GROUP)
+    sc = _nearest_code(np.abs(y).max(-1), 6 * E4M3)
+    s = E4M3[sc][..., None]
+    code = _nearest_code(np.abs(y), s[..., None] * E2M1)
+    code = np.where(s > 0, code, 0)
+    code = code + 8 * ((y < 0) & (code > 0))
+    code = code.reshape(*code.shape[:-2], -1).astype(np.uint8)
+    return code[..., 0::2] | (code[..., 1::2] << 4), sc.astype(np.uint8)
+
+
+def dequant_q4(packed, scales, scale: float = 1.0) -> np.ndarray:
+    """The values of packed codes and scale bytes, in float64 (exact)."""
+    packed = np.asarray(packed)
+    code = np.stack((packed & 15, packed >> 4), -1).reshape(*packed.shape[:-1], -1)
+    val = np.where(code & 8, -E2M1[code & 7], E2M1[code & 7])
+    return val * np.repeat(E4M3[np.asarray(scales)], Q4_GROUP, -1) * scale
+
+
+def visible_positions(kv_len: int, window=None, n_sink: int = 0) -> np.ndarray:
+    """The positions that a row of this length sees: all, or its last `window` and the first
+    n_sink."""
+    j = np.arange(max(int(kv_len), 0))
+    return j if not window else j[(j >= int(kv_len) - window) | (j < n_sink)]
+
+
+def _decode_visible(q, k_rows, v_rows, n_kv_heads, kv_len, scale, seq_of, window, n_sink):
+    """k_rows(s, g, J), v_rows(s, g, J): float64 rows of positions J."""
+    T, H, D = q.shape
+    G = H // n_kv_heads
+    out = np.zeros((T, H, D))
+    for t in range(T):
+        J = visible_positions(kv_len[t], window, n_sink)
+        if not len(J):
+            continue
+        s = t if seq_of is None else int(seq_of[t])
+        for g in range(n_kv_heads):
+            qg = np.asarray(q[t, g * G:(g + 1) * G], dtype=np.float64)
+            out[t, g * G:(g + 1) * G] = attend_positions(qg, k_rows(s, g, J), v_rows(s, g, J),
+                                                         scale)
+    return out
+
+
+def decode_q4(q, kq, vq, ksc, vsc, kv_len, scale, seq_of=None, k_scale=1.0, v_scale=1.0,
+              window=None, n_sink=0) -> np.ndarray:
+    """Decode attention over a 4-bit cache [n_seq][Hk][cap][..]."""
+    return _decode_visible(q, lambda s, g, J: dequant_q4(kq[s, g, J], ksc[s, g, J], k_scale),
+                           lambda s, g, J: dequant_q4(vq[s, g, J], vsc[s, g, J], v_scale),
+                           kq.shape[1], kv_len, scale, seq_of, window, n_sink)
+
+
+def decode_f16_window(q, k_cache, v_cache, kv_len, scale, window, n_sink=0,
+                      seq_of=None) -> np.ndarray:
+    """Decode attention over an f16 cache [n_seq][cap][Hk][D] through a window with sinks."""
+    return _decode_visible(q, lambda s, g, J: dequant_f16(k_cache[s, J, g]),
+                           lambda s, g, J: dequant_f16(v_cache[s, J, g]), k_cache.shape[2],
+                           kv_len, scale, seq_of, window, n_sink)
