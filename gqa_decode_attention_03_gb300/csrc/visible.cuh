@@ -6,21 +6,55 @@
 namespace gqa {
 
 // A row of length L sees [0, ns) and [w0, L), ns <= w0: the sinks that lie before the window, and
-// the window.  Without a window w0 is 0.  Entry i of the list is position i < ns ? i : i - ns + w0.
+// the window.  Without a window w0 is 0.
 struct Visible {
-  int L, w0, ns, n;  // n = ns + L - w0 entries
+  int L, w0, ns;
   __host__ __device__ Visible(int len, int window, int n_sink) : L(len) {
     w0 = window > 0 && window < len ? len - window : 0;
     ns = n_sink < w0 ? n_sink : w0;
-    n = ns + L - w0;
   }
-  __host__ __device__ int pos(int i) const { return i < ns ? i : i - ns + w0; }
+};
+
+// Those positions as tiles of TP: first the sinks' from position 0, then the window's from w0
+// rounded down to 16.  Tile i holds positions [start, start + TP), of which [lo, end) are seen.
+template <int TP>
+struct VisibleTiles {
+  Visible v;
+  int base, na, n;
+  __host__ __device__ explicit VisibleTiles(const Visible& vis) : v(vis) {
+    base = v.w0 & ~15;
+    na = (v.ns + TP - 1) / TP;
+    n = na + (v.L - base + TP - 1) / TP;
+  }
+  __host__ __device__ int start(int i) const { return i < na ? i * TP : base + (i - na) * TP; }
+  __host__ __device__ int lo(int i) const { return i < na ? 0 : v.w0; }
+  __host__ __device__ int end(int i) const { return i < na ? v.ns : v.L; }
 };
 
 struct VisibleParams {
-  PartialParams base;  // kc, vc, ksc, vsc hold the cache's pointers whatever its kind
+  PartialParams base;  // kc, vc, ksc, vsc hold the cache's pointers whatever its kind; chunk counts
+                       // tiles, n_valid is not used
   int window, n_sink;
   float k_scale, v_scale;  // 4-bit caches
 };
+
+constexpr int kQ4Tile = 32;  // positions of a tile of the 4-bit kernel
+
+// Row t's length and sequence; values out of range are flagged (by the thread that `flag` names)
+// and clamped, a row of a bad sequence sees nothing.
+__device__ __forceinline__ int visible_row(const PartialParams& p, int t, bool flag, int& s) {
+  int L = __ldg(p.kv_len + t), errbits = 0;
+  if (L < 0 || L > p.max_kv_len) {
+    errbits |= GQA_ERR_KVLEN_RANGE;
+    L = L < 0 ? 0 : p.max_kv_len;
+  }
+  s = p.seq_of ? __ldg(p.seq_of + t) : t;
+  if (s < 0 || s >= p.n_seq) {
+    errbits |= GQA_ERR_SEQ_RANGE;
+    L = 0;
+  }
+  if (errbits && flag) flag_error(p.err, errbits);
+  return L;
+}
 
 }  // namespace gqa

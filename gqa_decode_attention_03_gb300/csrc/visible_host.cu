@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <cstdlib>
 
 #include "host_util.h"
 #include "visible_dispatch.h"
@@ -11,18 +12,57 @@ namespace gqa {
 
 bool q4_scale_ok(float s);  // append_q4.cu
 
+// 4-bit caches: chunks of whole tiles, so many that about kQ4Waves CTAs per resident slot share
+// the rows at their longest, none shorter than two tiles a warp.
+constexpr int kQ4CtasPerSm = 3;
+constexpr int kQ4MaxChunkTiles = 64;
+constexpr int kQ4MinChunkTiles = 8;
+
 gqa_status plan_visible(int n_tok, int n_seq, int n_heads, int n_kv_heads, int head_dim,
                         int max_kv_len, int budget, int kind, int num_sms, gqa_plan* plan) {
-  (void)n_seq, (void)head_dim, (void)n_kv_heads, (void)num_sms, (void)kind;
+  (void)n_seq;
   if (budget == 0 || budget < -1)
     return fail(GQA_EINVAL, "budget %d: window + n_sink, or -1 for every position", budget);
   const int n = budget > 0 ? std::min(max_kv_len, budget) : max_kv_len;
-  plan->chunk = std::max(n, 1);
-  plan->n_split = 1;
-  plan->tile = 1;
-  plan->grid_x = n_heads;
-  plan->grid_y = n_tok;
-  plan->grid_z = 1;
+  if (kind == GQA_KIND_F16_WINDOW) {
+    plan->chunk = std::max(n, 1);
+    plan->n_split = 1;
+    plan->tile = 1;
+    plan->grid_x = n_heads;
+    plan->grid_y = n_tok;
+    plan->grid_z = 1;
+    return GQA_OK;
+  }
+  if (num_sms <= 0) {
+    gqa_status st = GQA_OK;
+    num_sms = current_sm_count(&st);
+    if (num_sms <= 0) return st != GQA_OK ? st : fail(GQA_ECUDA, "no SM count");
+  }
+  const int group = n_heads / n_kv_heads;
+  int hs = 1;  // CTAs of a KV head's query heads, at most 8 each
+  while (group % hs || group / hs > 8) ++hs;
+  // the sinks' last tile and the window's first one may be partly seen
+  const long long tiles = ((long long)n + kQ4Tile - 1) / kQ4Tile + (budget > 0 ? 2 : 0);
+  const long long units = (long long)n_tok * n_kv_heads * hs;
+  const long long slots = (long long)kQ4CtasPerSm * num_sms;
+  long long chunk = (std::max(units, 1LL) * tiles + slots - 1) / slots;
+  chunk = std::min<long long>(std::max<long long>(chunk, kQ4MinChunkTiles), kQ4MaxChunkTiles);
+  if (const char* f = std::getenv("GQA_FORCE_CHUNK"))
+    if (std::atoi(f) > 0) chunk = (std::atoi(f) + kQ4Tile - 1) / kQ4Tile;
+  const long long n_split = std::max(1LL, (tiles + chunk - 1) / chunk);
+  if (n_split > (1 << 30) || (long long)n_kv_heads * hs > 65535)
+    return fail(GQA_EUNSUPPORTED, "too many chunks or heads for one launch");
+  plan->chunk = (int)(chunk * kQ4Tile);
+  plan->n_split = (int)n_split;
+  plan->tile = kQ4Tile;
+  plan->grid_x = (int)n_split;
+  plan->grid_y = n_kv_heads * hs;
+  plan->grid_z = n_tok;
+  plan->merge = n_split > 1 ? 1 : 0;
+  if (plan->merge) {
+    const size_t cnt = ((size_t)n_tok * plan->grid_y * sizeof(uint32_t) + 255) / 256 * 256;
+    plan->ws_bytes = cnt + (size_t)n_tok * n_split * n_heads * (head_dim + 2) * sizeof(float);
+  }
   return GQA_OK;
 }
 
@@ -89,10 +129,16 @@ static gqa_status visible_common(int kind, const float* q, const void* kc, const
   p.group = n_heads / n_kv_heads;
   p.cache_cap = cache_cap;
   p.max_kv_len = max_len;
-  p.chunk = plan.chunk;
+  p.chunk = plan.chunk / plan.tile;
   p.n_split = plan.n_split;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.merge = plan.merge;
+  p.head_split = std::max(1, plan.grid_y / n_kv_heads);
+  if (plan.merge) {  // ws = [arrival counters][partials]
+    const size_t cnt = ((size_t)n_tok * plan.grid_y * sizeof(uint32_t) + 255) / 256 * 256;
+    p.counters = static_cast<unsigned int*>(ws);
+    p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + cnt);
+  }
   p.gate = gate;
   p.gate_stride = gate ? gate_stride : 0;
   vp.window = window;

@@ -4,7 +4,6 @@
 // of q and of the accumulator, the running maximum and sum are kept per warp in fp32 and the four
 // states meet in shared memory.
 #include "dispatch.h"
-#include "q4_common.cuh"
 #include "visible.cuh"
 #include "visible_dispatch.h"
 
@@ -12,49 +11,24 @@ namespace gqa {
 
 constexpr int kSimpleWarps = 4;
 
-template <int D, bool Q4>
-__device__ __forceinline__ void simple_row(const VisibleParams& vp, bool v, int s, int g, int pos,
-                                           int lane, float (&f)[D / 32]) {
-  const PartialParams& p = vp.base;
-  if constexpr (Q4) {
-    const size_t row = ((size_t)s * p.n_kv_heads + g) * p.cache_cap + pos;
-    const uint8_t* c = static_cast<const uint8_t*>(v ? p.vc : p.kc) + row * (D / 2);
-    const uint8_t* sc = reinterpret_cast<const uint8_t*>(v ? p.vsc : p.ksc) + row * (D / 16);
+template <int D>
+__device__ __forceinline__ void simple_row(const PartialParams& p, const void* cache, int s, int g,
+                                           int pos, int lane, float (&f)[D / 32]) {
+  const __half* c = static_cast<const __half*>(cache) +
+                    (((size_t)s * p.cache_cap + pos) * p.n_kv_heads + g) * D;
 #pragma unroll
-    for (int k = 0; k < D / 32; k += 2) {
-      const int d = lane * (D / 32) + k;
-      const uint32_t h = e2m1x2_to_f16x2(c[d / 2]);
-      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      const float sf = e4m3_to_f32(sc[d / 16]) * (v ? vp.v_scale : vp.k_scale);
-      f[k] = x.x * sf;
-      f[k + 1] = x.y * sf;
-    }
-  } else {
-    const __half* c = static_cast<const __half*>(v ? p.vc : p.kc) +
-                      (((size_t)s * p.cache_cap + pos) * p.n_kv_heads + g) * D;
-#pragma unroll
-    for (int k = 0; k < D / 32; ++k) f[k] = __half2float(c[lane * (D / 32) + k]);
-  }
+  for (int k = 0; k < D / 32; ++k) f[k] = __half2float(c[lane * (D / 32) + k]);
 }
 
-template <int D, bool Q4>
+template <int D>
 __global__ void __launch_bounds__(32 * kSimpleWarps) visible_simple_kernel(const VisibleParams vp) {
   constexpr int DPL = D / 32;
   const PartialParams& p = vp.base;
   __shared__ float mg[kSimpleWarps][D + 2];
   const int h = blockIdx.x, t = blockIdx.y, g = h / p.group;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int L = __ldg(p.kv_len + t), errbits = 0;
-  if (L < 0 || L > p.max_kv_len) {
-    errbits |= GQA_ERR_KVLEN_RANGE;
-    L = L < 0 ? 0 : p.max_kv_len;
-  }
-  const int s = p.seq_of ? __ldg(p.seq_of + t) : t;
-  if (s < 0 || s >= p.n_seq) {
-    errbits |= GQA_ERR_SEQ_RANGE;
-    L = 0;
-  }
-  if (errbits && h == 0 && threadIdx.x == 0) flag_error(p.err, errbits);
+  int s = 0;
+  const int L = visible_row(p, t, h == 0 && threadIdx.x == 0, s);
   const Visible vis(L, vp.window, vp.n_sink);
   float q[DPL], o[DPL], f[DPL];
 #pragma unroll
@@ -63,9 +37,9 @@ __global__ void __launch_bounds__(32 * kSimpleWarps) visible_simple_kernel(const
     o[k] = 0.f;
   }
   float m = -INFINITY, l = 0.f;
-  for (int i = warp; i < vis.n; i += kSimpleWarps) {
-    const int pos = vis.pos(i);
-    simple_row<D, Q4>(vp, false, s, g, pos, lane, f);
+  for (int i = warp; i < vis.ns + L - vis.w0; i += kSimpleWarps) {
+    const int pos = i < vis.ns ? i : i - vis.ns + vis.w0;
+    simple_row<D>(p, p.kc, s, g, pos, lane, f);
     float x = 0.f;
 #pragma unroll
     for (int k = 0; k < DPL; ++k) x = fmaf(q[k], f[k], x);
@@ -74,7 +48,7 @@ __global__ void __launch_bounds__(32 * kSimpleWarps) visible_simple_kernel(const
     const float corr = m == -INFINITY ? 0.f : fast_exp2(m - mn), w = fast_exp2(x - mn);
     m = mn;
     l = l * corr + w;
-    simple_row<D, Q4>(vp, true, s, g, pos, lane, f);
+    simple_row<D>(p, p.vc, s, g, pos, lane, f);
 #pragma unroll
     for (int k = 0; k < DPL; ++k) o[k] = fmaf(w, f[k], o[k] * corr);
   }
@@ -97,24 +71,16 @@ __global__ void __launch_bounds__(32 * kSimpleWarps) visible_simple_kernel(const
   }
 }
 
-template <bool Q4>
-static cudaError_t launch_simple(int head_dim, const VisibleParams& vp, cudaStream_t s) {
-  const dim3 grid(vp.base.n_heads, vp.base.n_tok);
-  if (head_dim == 64)
-    visible_simple_kernel<64, Q4><<<grid, 32 * kSimpleWarps, 0, s>>>(vp);
-  else if (head_dim == 128)
-    visible_simple_kernel<128, Q4><<<grid, 32 * kSimpleWarps, 0, s>>>(vp);
-  else
-    visible_simple_kernel<256, Q4><<<grid, 32 * kSimpleWarps, 0, s>>>(vp);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_q4(int head_dim, const VisibleParams& vp, const gqa_plan&, cudaStream_t s) {
-  return launch_simple<true>(head_dim, vp, s);
-}
 cudaError_t launch_f16_window(int head_dim, const VisibleParams& vp, const gqa_plan&,
                               cudaStream_t s) {
-  return launch_simple<false>(head_dim, vp, s);
+  const dim3 grid(vp.base.n_heads, vp.base.n_tok);
+  if (head_dim == 64)
+    visible_simple_kernel<64><<<grid, 32 * kSimpleWarps, 0, s>>>(vp);
+  else if (head_dim == 128)
+    visible_simple_kernel<128><<<grid, 32 * kSimpleWarps, 0, s>>>(vp);
+  else
+    visible_simple_kernel<256><<<grid, 32 * kSimpleWarps, 0, s>>>(vp);
+  return cudaGetLastError();
 }
 
 }  // namespace gqa
