@@ -140,10 +140,11 @@ __global__ void __launch_bounds__(kQ4Threads)
 
 // 8 codes times scale s -> 8 values.
 __device__ __forceinline__ void q4_values(uint32_t codes, float s, float (&f)[8]) {
+  uint32_t h[4];
+  e2m1x8_to_f16x2(codes, h);
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
-    const uint32_t h = e2m1x2_to_f16x2(codes >> (8 * b));
-    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h[b]));
     f[2 * b] = x.x * s;
     f[2 * b + 1] = x.y * s;
   }

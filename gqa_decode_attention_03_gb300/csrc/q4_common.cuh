@@ -18,15 +18,16 @@ __device__ __forceinline__ float e4m3_to_f32(uint32_t b) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>((b & 0x7fu) << 7))) * 256.f;
 }
 
-// Two e2m1 codes (the low byte of x, low nibble first) -> their values as an f16x2.
-__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t x) {
-  uint32_t r;
+// Eight e2m1 codes (a word, low nibble first) -> their values as four f16x2.
+__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t (&h)[4]) {
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t}"
-      : "=r"(r)
-      : "r"(x));
-  return r;
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
 }
 
 // The sequence holding row r of a ragged batch: the last s with row_off[s] <= r, or -1.  All 32

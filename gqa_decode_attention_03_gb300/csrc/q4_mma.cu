@@ -33,7 +33,7 @@ struct Q4Cfg {
   static constexpr int NW = 4;                      // warps
   static constexpr int RB = D / 2, SB = D / 16;     // bytes of a position's codes and scales
   static constexpr int TP = kQ4Tile;                // positions of a tile
-  static constexpr int NB = TP / 16;
+  static constexpr int NB = TP / 16, NTK = TP / 8;  // 16-position blocks, n-tiles of q.k
   static constexpr int STAGE = 2 * TP * (RB + SB);  // [K codes][V codes][K scales][V scales]
   static constexpr int NST = D == 64 ? 6 : (D == 128 ? 4 : 3);
   static constexpr int MIN_CTAS = D == 256 ? 2 : 3;
@@ -170,102 +170,108 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D>::NW, Q4Cfg<D>::MIN_CTAS)
     const uint8_t* ssk = sv + C::TP * C::RB;
     const uint8_t* ssv = ssk + C::TP * C::SB;
     const int lo = tiles.lo(i) - tiles.start(i), hi = tiles.end(i) - tiles.start(i);
+    // -- S = Q . K^T of the tile's 32 positions, four n-tiles
+    float sc[C::NTK][4];
+#pragma unroll
+    for (int nt = 0; nt < C::NTK; ++nt) {
+      const int r = 8 * nt + krow;
+      uint32_t kw[C::KW];
+      __half2 ks2[C::KW / 2];  // one scale per two words, broadcast
+      if constexpr (D == 64) {
+        const uint2 u = *reinterpret_cast<const uint2*>(sk + r * C::RB + 8 * tig);
+        kw[0] = u.x;
+        kw[1] = u.y;
+        const uint32_t b0 = ssk[r * C::SB + tig];
+        ks2[0] = e4m3x2_to_f16x2(b0 | b0 << 16);
+      } else {
+#pragma unroll
+        for (int k = 0; k < C::KW / 4; ++k) {
+          const uint4 u = *reinterpret_cast<const uint4*>(sk + r * C::RB + 64 * k + 16 * tig);
+          kw[4 * k] = u.x;
+          kw[4 * k + 1] = u.y;
+          kw[4 * k + 2] = u.z;
+          kw[4 * k + 3] = u.w;
+          const uint32_t b2 =
+              *reinterpret_cast<const uint16_t*>(ssk + r * C::SB + 8 * k + 2 * tig);
+          const __half2 h = e4m3x2_to_f16x2(__byte_perm(b2, 0, 0x4140));
+          ks2[2 * k] = __low2half2(h);
+          ks2[2 * k + 1] = __high2half2(h);
+        }
+      }
+      sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+#pragma unroll
+      for (int w = 0; w < C::KW; ++w) {
+        uint32_t h[4];
+        e2m1x8_to_f16x2(kw[w], h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = mul_h2(h[e], ks2[w / 2]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if constexpr (C::QSMEM) {
+            const uint4 a4 = qf[(2 * w + e) * 32];
+            const uint32_t a[4] = {a4.x, a4.y, a4.z, a4.w};
+            mma_f16(sc[nt], a, h[2 * e], h[2 * e + 1]);
+          } else {
+            mma_f16(sc[nt], qa[2 * w + e], h[2 * e], h[2 * e + 1]);
+          }
+        }
+      }
+    }
+    // -- head gid's scores at positions 8 nt + 4 j + (tig ^ 3 j)
+    float x[C::NTK][2];
+    float mt = -INFINITY;
+#pragma unroll
+    for (int nt = 0; nt < C::NTK; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) x[nt][j] = (sc[nt][j] + sc[nt][2 + j]) * sm;
+    if (lo > 0 || hi < C::TP) {
+#pragma unroll
+      for (int nt = 0; nt < C::NTK; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int r = 8 * nt + 4 * j + (tig ^ (3 * j));
+          if (r < lo || r >= hi) x[nt][j] = -INFINITY;
+        }
+    }
+#pragma unroll
+    for (int nt = 0; nt < C::NTK; ++nt) mt = fmaxf(mt, fmaxf(x[nt][0], x[nt][1]));
+    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
+    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
+    // -- the running maximum moves only when a tile exceeds it by 2^8 (weights <= 256)
+    const bool grow = mt > m_run + C::RESCALE_LOG2;
+    if (__any_sync(0xffffffffu, grow)) {
+      const float m_new = grow ? mt : m_run;
+      const float corr = m_run == -INFINITY ? 0.f : fast_exp2(m_run - m_new);
+      m_run = m_new;
+      l_run *= corr;
+#pragma unroll
+      for (int n = 0; n < C::NT; ++n) {
+        o[n][0] *= corr;
+        o[n][1] *= corr;
+        o[n][2] *= corr;
+        o[n][3] *= corr;
+      }
+    }
+    const float mu = m_run == -INFINITY ? 0.f : m_run;
+#pragma unroll
+    for (int nt = 0; nt < C::NTK; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        x[nt][j] = fast_exp2(x[nt][j] - mu);  // 0 where masked
+        l_run += x[nt][j];
+      }
+    // -- O += P . V, 16 positions at a time.  Codes of a masked position are finite whatever they
+    //    hold, and weigh 0; behind the positions that were copied the stage holds older codes.
 #pragma unroll
     for (int b = 0; b < C::NB; ++b) {
-      const int r0 = 16 * b;
-      if (r0 >= hi || r0 + 16 <= lo) continue;
-      // -- S = Q . K^T, two accumulator chains per n-tile
-      float sc[2][2][4];
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        const int r = r0 + 8 * nt + krow;
-        uint32_t kw[C::KW];
-        __half2 ks2[C::KW / 2];  // one scale per two words, broadcast
-        if constexpr (D == 64) {
-          const uint2 u = *reinterpret_cast<const uint2*>(sk + r * C::RB + 8 * tig);
-          kw[0] = u.x;
-          kw[1] = u.y;
-          const uint32_t b0 = ssk[r * C::SB + tig];
-          ks2[0] = e4m3x2_to_f16x2(b0 | b0 << 16);
-        } else {
-#pragma unroll
-          for (int k = 0; k < C::KW / 4; ++k) {
-            const uint4 u = *reinterpret_cast<const uint4*>(sk + r * C::RB + 64 * k + 16 * tig);
-            kw[4 * k] = u.x;
-            kw[4 * k + 1] = u.y;
-            kw[4 * k + 2] = u.z;
-            kw[4 * k + 3] = u.w;
-            const uint32_t b2 =
-                *reinterpret_cast<const uint16_t*>(ssk + r * C::SB + 8 * k + 2 * tig);
-            const __half2 h = e4m3x2_to_f16x2(__byte_perm(b2, 0, 0x4140));
-            ks2[2 * k] = __low2half2(h);
-            ks2[2 * k + 1] = __high2half2(h);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[nt][0][e] = sc[nt][1][e] = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < C::KS; ++ks) {
-          const uint32_t w = kw[ks / 2];
-          const uint32_t b0 = mul_h2(e2m1x2_to_f16x2(w >> (16 * (ks & 1))), ks2[ks / 4]);
-          const uint32_t b1 = mul_h2(e2m1x2_to_f16x2(w >> (16 * (ks & 1) + 8)), ks2[ks / 4]);
-          if constexpr (C::QSMEM) {
-            const uint4 a4 = qf[ks * 32];
-            const uint32_t a[4] = {a4.x, a4.y, a4.z, a4.w};
-            mma_f16(sc[nt][ks & 1], a, b0, b1);
-          } else {
-            mma_f16(sc[nt][ks & 1], qa[ks], b0, b1);
-          }
-        }
-      }
-      // -- head gid's scores at positions r0 + 4 (2 nt + j) + (tig ^ 3 j)
-      float x[2][2];
-      float mt = -INFINITY;
-      const bool whole = r0 >= lo && r0 + 16 <= hi;
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int r = r0 + 8 * nt + 4 * j + (tig ^ (3 * j));
-          const float y = ((sc[nt][0][j] + sc[nt][1][j]) + (sc[nt][0][2 + j] + sc[nt][1][2 + j])) * sm;
-          x[nt][j] = whole || (r >= lo && r < hi) ? y : -INFINITY;
-          mt = fmaxf(mt, x[nt][j]);
-        }
-      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
-      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
-      // -- the running maximum moves only when a block exceeds it by 2^8 (weights <= 256)
-      const bool grow = mt > m_run + C::RESCALE_LOG2;
-      if (__any_sync(0xffffffffu, grow)) {
-        const float m_new = grow ? mt : m_run;
-        const float corr = m_run == -INFINITY ? 0.f : fast_exp2(m_run - m_new);
-        m_run = m_new;
-        l_run *= corr;
-#pragma unroll
-        for (int n = 0; n < C::NT; ++n) {
-          o[n][0] *= corr;
-          o[n][1] *= corr;
-          o[n][2] *= corr;
-          o[n][3] *= corr;
-        }
-      }
-      const float mu = m_run == -INFINITY ? 0.f : m_run;
-      float pr[2][2];
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          pr[nt][j] = fast_exp2(x[nt][j] - mu);  // 0 where masked
-          l_run += pr[nt][j];
-        }
       uint32_t pa[4];
-      split_hi_lo(pr[0][0], pr[0][1], pa[0], pa[1]);
-      split_hi_lo(pr[1][0], pr[1][1], pa[2], pa[3]);
-      // -- O += P . V: codes of a masked position are finite whatever they hold, and weigh 0
+      split_hi_lo(x[2 * b][0], x[2 * b][1], pa[0], pa[1]);
+      split_hi_lo(x[2 * b + 1][0], x[2 * b + 1][1], pa[2], pa[3]);
       uint32_t vw[4][C::VW];
       uint32_t vs[4];  // scales: one byte, or two at D = 256
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int r = r0 + 4 * j + (tig ^ (3 * (j & 1)));
+        const int r = 16 * b + 4 * j + (tig ^ (3 * (j & 1)));
         const uint8_t* src = sv + r * C::RB + gid * (D / 16);
         if constexpr (D == 64) {
           vw[j][0] = *reinterpret_cast<const uint32_t*>(src);
@@ -288,8 +294,8 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D>::NW, Q4Cfg<D>::MIN_CTAS)
       for (int h = 0; h < (D == 256 ? 2 : 1); ++h) {  // scale groups of the thread's dims
         __half2 s01, s23;
         if constexpr (D == 256) {
-          s01 = e4m3x2_to_f16x2(__byte_perm(vs[0], vs[1], h ? 0x5511 : 0x4400) & 0x00ff00ffu);
-          s23 = e4m3x2_to_f16x2(__byte_perm(vs[2], vs[3], h ? 0x5511 : 0x4400) & 0x00ff00ffu);
+          s01 = e4m3x2_to_f16x2(__byte_perm(vs[0], vs[1], h ? 0x5511 : 0x4400));
+          s23 = e4m3x2_to_f16x2(__byte_perm(vs[2], vs[3], h ? 0x5511 : 0x4400));
         } else {
           s01 = e4m3x2_to_f16x2(vs[0] | vs[1] << 16);
           s23 = e4m3x2_to_f16x2(vs[2] | vs[3] << 16);
@@ -299,16 +305,15 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D>::NW, Q4Cfg<D>::MIN_CTAS)
         for (int w = 0; w < WG; ++w) {
           const int ww = WG * h + w;
           constexpr uint32_t M = 0x0f0f0f0fu;
-          const uint32_t e01 = (vw[0][ww] & M) | ((vw[1][ww] << 4) & ~M);  // even dims
-          const uint32_t o01 = ((vw[0][ww] >> 4) & M) | (vw[1][ww] & ~M);  // odd dims
-          const uint32_t e23 = (vw[2][ww] & M) | ((vw[3][ww] << 4) & ~M);
-          const uint32_t o23 = ((vw[2][ww] >> 4) & M) | (vw[3][ww] & ~M);
+          uint32_t e01[4], o01[4], e23[4], o23[4];  // even and odd dims of two positions
+          e2m1x8_to_f16x2((vw[0][ww] & M) | ((vw[1][ww] << 4) & ~M), e01);
+          e2m1x8_to_f16x2(((vw[0][ww] >> 4) & M) | (vw[1][ww] & ~M), o01);
+          e2m1x8_to_f16x2((vw[2][ww] & M) | ((vw[3][ww] << 4) & ~M), e23);
+          e2m1x8_to_f16x2(((vw[2][ww] >> 4) & M) | (vw[3][ww] & ~M), o23);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            mma_f16(o[8 * ww + 2 * k], pa, mul_h2(e2m1x2_to_f16x2(e01 >> (8 * k)), s01),
-                    mul_h2(e2m1x2_to_f16x2(e23 >> (8 * k)), s23));
-            mma_f16(o[8 * ww + 2 * k + 1], pa, mul_h2(e2m1x2_to_f16x2(o01 >> (8 * k)), s01),
-                    mul_h2(e2m1x2_to_f16x2(o23 >> (8 * k)), s23));
+            mma_f16(o[8 * ww + 2 * k], pa, mul_h2(e01[k], s01), mul_h2(e23[k], s23));
+            mma_f16(o[8 * ww + 2 * k + 1], pa, mul_h2(o01[k], s01), mul_h2(o23[k], s23));
           }
         }
       }
