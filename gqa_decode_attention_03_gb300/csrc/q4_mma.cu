@@ -173,47 +173,59 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D>::NW, Q4Cfg<D>::MIN_CTAS)
     // -- S = Q . K^T of the tile's 32 positions, four n-tiles
     float sc[C::NTK][4];
 #pragma unroll
-    for (int nt = 0; nt < C::NTK; ++nt) {
-      const int r = 8 * nt + krow;
-      uint32_t kw[C::KW];
-      __half2 ks2[C::KW / 2];  // one scale per two words, broadcast
-      if constexpr (D == 64) {
-        const uint2 u = *reinterpret_cast<const uint2*>(sk + r * C::RB + 8 * tig);
-        kw[0] = u.x;
-        kw[1] = u.y;
-        const uint32_t b0 = ssk[r * C::SB + tig];
-        ks2[0] = e4m3x2_to_f16x2(b0 | b0 << 16);
-      } else {
+    for (int nt = 0; nt < C::NTK; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
 #pragma unroll
-        for (int k = 0; k < C::KW / 4; ++k) {
+    for (int k = 0; k < (C::KW + 3) / 4; ++k) {  // a thread's 16-byte runs of codes
+      constexpr int W = cmin(C::KW, 4);
+      uint32_t kw[C::NTK][W];
+      __half2 ks2[C::NTK][W / 2];  // one scale per two words, broadcast
+#pragma unroll
+      for (int nt = 0; nt < C::NTK; ++nt) {
+        const int r = 8 * nt + krow;
+        if constexpr (D == 64) {
+          const uint2 u = *reinterpret_cast<const uint2*>(sk + r * C::RB + 8 * tig);
+          kw[nt][0] = u.x;
+          kw[nt][1] = u.y;
+          const uint32_t b0 = ssk[r * C::SB + tig];
+          ks2[nt][0] = e4m3x2_to_f16x2(b0 | b0 << 16);
+        } else {
           const uint4 u = *reinterpret_cast<const uint4*>(sk + r * C::RB + 64 * k + 16 * tig);
-          kw[4 * k] = u.x;
-          kw[4 * k + 1] = u.y;
-          kw[4 * k + 2] = u.z;
-          kw[4 * k + 3] = u.w;
+          kw[nt][0] = u.x;
+          kw[nt][1] = u.y;
+          kw[nt][2] = u.z;
+          kw[nt][3] = u.w;
           const uint32_t b2 =
               *reinterpret_cast<const uint16_t*>(ssk + r * C::SB + 8 * k + 2 * tig);
           const __half2 h = e4m3x2_to_f16x2(__byte_perm(b2, 0, 0x4140));
-          ks2[2 * k] = __low2half2(h);
-          ks2[2 * k + 1] = __high2half2(h);
+          ks2[nt][0] = __low2half2(h);
+          ks2[nt][1] = __high2half2(h);
         }
       }
-      sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
 #pragma unroll
-      for (int w = 0; w < C::KW; ++w) {
-        uint32_t h[4];
-        e2m1x8_to_f16x2(kw[w], h);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = mul_h2(h[e], ks2[w / 2]);
+      for (int w = 0; w < W; ++w) {
+        uint32_t a[2][4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+          const int ks = 2 * (4 * k + w) + e;
           if constexpr (C::QSMEM) {
-            const uint4 a4 = qf[(2 * w + e) * 32];
-            const uint32_t a[4] = {a4.x, a4.y, a4.z, a4.w};
-            mma_f16(sc[nt], a, h[2 * e], h[2 * e + 1]);
+            const uint4 a4 = qf[ks * 32];
+            a[e][0] = a4.x;
+            a[e][1] = a4.y;
+            a[e][2] = a4.z;
+            a[e][3] = a4.w;
           } else {
-            mma_f16(sc[nt], qa[2 * w + e], h[2 * e], h[2 * e + 1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[e][i] = qa[ks][i];
           }
+        }
+#pragma unroll
+        for (int nt = 0; nt < C::NTK; ++nt) {
+          uint32_t h[4];
+          e2m1x8_to_f16x2(kw[nt][w], h);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[e] = mul_h2(h[e], ks2[nt][w / 2]);
+          mma_f16(sc[nt], a[0], h[0], h[1]);
+          mma_f16(sc[nt], a[1], h[2], h[3]);
         }
       }
     }
