@@ -63,16 +63,6 @@ int current_sm_count(gqa_status* st) {
   return n;
 }
 
-}  // namespace gqa
-
-namespace {
-
-using gqa::aligned16;
-using gqa::check_shape;
-using gqa::cuda_fail;
-using gqa::current_sm_count;
-using gqa::fail;
-
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static std::once_flag once;
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -86,6 +76,39 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   });
   return fn;
 }
+
+// The 3-D maps [row][n_kv_heads][head_dim] of an f16 cache, in boxes of 64 dims x 1 head x `tile`
+// rows with the 128-byte swizzle.
+gqa_status encode_f16_cache(const void* kc, const void* vc, int n_seq, int64_t cache_cap,
+                            int n_kv_heads, int head_dim, int tile, CUtensorMap* tk,
+                            CUtensorMap* tv) {
+  auto encode = tensor_map_encoder();
+  if (!encode) return fail(GQA_ECUDA, "cuTensorMapEncodeTiled is unavailable");
+  const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)n_kv_heads,
+                              (cuuint64_t)n_seq * (cuuint64_t)cache_cap};
+  const cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2,
+                                 (cuuint64_t)head_dim * 2 * (cuuint64_t)n_kv_heads};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)tile};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  for (int i = 0; i < 2; ++i) {
+    CUresult r = encode(i ? tv : tk, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                        const_cast<void*>(i ? vc : kc), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(GQA_ECUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  }
+  return GQA_OK;
+}
+
+}  // namespace gqa
+
+namespace {
+
+using gqa::aligned16;
+using gqa::check_shape;
+using gqa::cuda_fail;
+using gqa::current_sm_count;
+using gqa::fail;
 
 int env_int(const char* name) {
   const char* v = std::getenv(name);
@@ -506,21 +529,8 @@ gqa_status decode_common(int kind, const float* q, const void* kc, const void* v
   std::memset(&tv, 0, sizeof tv);
   std::memset(&tq, 0, sizeof tq);
   if (kind == GQA_KIND_F16) {
-    auto encode = tensor_map_encoder();
-    if (!encode) return fail(GQA_ECUDA, "cuTensorMapEncodeTiled is unavailable");
-    const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)n_kv_heads,
-                                (cuuint64_t)n_seq * (cuuint64_t)cache_cap};
-    const cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2,
-                                   (cuuint64_t)head_dim * 2 * (cuuint64_t)n_kv_heads};
-    const cuuint32_t box[3] = {64, 1, (cuuint32_t)plan.tile};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    for (int i = 0; i < 2; ++i) {
-      CUresult r = encode(i ? &tv : &tk, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-                          const_cast<void*>(i ? vc : kc), dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-      if (r != CUDA_SUCCESS) return fail(GQA_ECUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
-    }
+    st = gqa::encode_f16_cache(kc, vc, n_seq, cache_cap, n_kv_heads, head_dim, plan.tile, &tk, &tv);
+    if (st != GQA_OK) return st;
     if (plan.row_group > 1 && gqa::rows_on_umma()) {
       // the tcgen05 row kernel stages a group's fp32 q [rows][G heads][D] with one copy: box
       // D x G x 64 / G rows (rows past n_tok read as zeros)
@@ -529,7 +539,8 @@ gqa_status decode_common(int kind, const float* q, const void* kc, const void* v
       const cuuint64_t qstr[2] = {(cuuint64_t)head_dim * 4,
                                   (cuuint64_t)head_dim * 4 * (cuuint64_t)n_heads};
       const cuuint32_t qbox[3] = {(cuuint32_t)head_dim, (cuuint32_t)G, (cuuint32_t)(64 / G)};
-      CUresult r = encode(&tq, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<float*>(q), qdims,
+      const cuuint32_t estr[3] = {1, 1, 1};
+      CUresult r = gqa::tensor_map_encoder()(&tq, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<float*>(q), qdims,
                           qstr, qbox, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                           CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);

@@ -72,6 +72,8 @@ struct PartialParams {
                            // one thread-block cluster (dims (n_split, 1, 1)) and merge through
                            // distributed shared memory instead of the arrival counters (the
                            // host sets 1 where the f16 kernel may, the launcher the size)
+  int window, n_sink;      // calls with a visible set (visible.cuh): the window (0: none) and the
+                           // first positions that stay visible; chunk then counts tiles
 };
 
 // The sigmoid output gate that both pages apply to the merged row (qsa2.metal, qsa_merge2;
@@ -392,11 +394,12 @@ inline int cluster_attrs(cudaLaunchAttribute* at, int cluster, int pdl) {
 
 // ------------------------------------------------------------------------------ producers
 
-// f16: lane 0 streams the chunk's K/V tiles by TMA into the stage ring.
-template <class C>
+// f16: lane 0 streams the chunk's K/V tiles by TMA into the stage ring; tile i starts at cache row
+// z_of(i).
+template <class C, class Z>
 __device__ __forceinline__ void produce_tma(const CUtensorMap* tmK, const CUtensorMap* tmV,
                                             uint8_t* stages, uint64_t* full, uint64_t* empty,
-                                            int ntiles, int g, int z0, int32_t* err) {
+                                            int ntiles, int g, const Z& z_of, int32_t* err) {
   tma_prefetch_desc(tmK);
   tma_prefetch_desc(tmV);
   int issued = 0;
@@ -410,7 +413,7 @@ __device__ __forceinline__ void produce_tma(const CUtensorMap* tmK, const CUtens
     mbar_arrive_expect_tx(&full[st], C::KV_BYTES);
     uint8_t* sk = stages + st * C::STAGE_BYTES;
     uint8_t* sv = sk + C::NBOX * C::BOX_BYTES;
-    const int z = z0 + i * C::TP;
+    const int z = z_of(i);
 #pragma unroll
     for (int b = 0; b < C::NBOX; ++b) {
       tma_load_3d(sk + b * C::BOX_BYTES, tmK, b * 64, g, z, &full[st]);
@@ -590,8 +593,9 @@ __global__ void __launch_bounds__(Cfg<K, D, GW, NPS>::MAX_THREADS, Cfg<K, D, GW,
   if (warp == ncw) {  // ---- producer warp
     if constexpr (K == Kind::F16) {
       if (lane == 0)
-        produce_tma<C>(&tmK, &tmV, stages, full, empty, ntiles, g,
-                       s * static_cast<int>(p.cache_cap) + c0, p.err);
+        produce_tma<C>(
+            &tmK, &tmV, stages, full, empty, ntiles, g,
+            [&](int i) { return s * static_cast<int>(p.cache_cap) + c0 + i * C::TP; }, p.err);
     } else {
       produce_gather<C, D>(p, stages, full, empty, ntiles, t, g, s, L, c0, c1, lane);
     }

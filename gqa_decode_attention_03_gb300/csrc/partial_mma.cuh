@@ -26,6 +26,7 @@
 #pragma once
 
 #include "partial_kernel.cuh"
+#include "visible.cuh"
 
 namespace gqa {
 
@@ -94,7 +95,7 @@ __device__ __forceinline__ void split_hi_lo(float a, float b, uint32_t& hi, uint
   lo = h2_bits(__floats2half2_rn(a - hf.x, b - hf.y));
 }
 
-template <int D, int NHG>
+template <int D, int NHG, bool WIN = false>
 __global__ void __launch_bounds__(MmaCfg<D, NHG>::MAX_THREADS, MmaCfg<D, NHG>::MIN_BLOCKS)
     partial_mma_kernel(const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const PartialParams p) {
@@ -127,15 +128,18 @@ __global__ void __launch_bounds__(MmaCfg<D, NHG>::MAX_THREADS, MmaCfg<D, NHG>::M
     errbits |= GQA_ERR_SEQ_RANGE;
     L = 0;
   }
-  // the row's chunks: ceil(L / chunk) of them, of p.chunk positions each (the last one shorter)
-  const int nchunks = (L + p.chunk - 1) / p.chunk;
+  // the row's chunks: ceil(L / chunk) of them, of p.chunk positions each (the last one shorter);
+  // WIN: of p.chunk tiles of the row's list
+  const VisibleTiles<C::TP, 1> tiles(Visible(L, p.window, p.n_sink));  // WIN
+  const int len = WIN ? tiles.n : L;
+  const int nchunks = (len + p.chunk - 1) / p.chunk;
   const int c0 = c * p.chunk;
-  const int c1 = min(c0 + p.chunk, L);
+  const int c1 = min(c0 + p.chunk, len);
   if (c == 0 && g == 0 && threadIdx.x == 0) {
     if (errbits) flag_error(p.err, errbits);
-    if (p.merge) p.n_valid[t] = nchunks;
+    if (p.merge && !WIN) p.n_valid[t] = nchunks;
   }
-  if (c0 >= L) {
+  if (c0 >= len) {
     if (c == 0)  // empty context: zeros (flash_attention.metal, seq_len == 0), split or not
       for (int i = threadIdx.x; i < G * D; i += blockDim.x)
         p.out[((size_t)t * p.n_heads + g * G + i / D) * D + i % D] = 0.f;
@@ -145,7 +149,7 @@ __global__ void __launch_bounds__(MmaCfg<D, NHG>::MAX_THREADS, MmaCfg<D, NHG>::M
     }
     return;
   }
-  const int ntiles = (c1 - c0 + C::TP - 1) / C::TP;
+  const int ntiles = WIN ? c1 - c0 : (c1 - c0 + C::TP - 1) / C::TP;
 
   const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
   uint8_t* stages = smem_raw + pad;
@@ -162,8 +166,13 @@ __global__ void __launch_bounds__(MmaCfg<D, NHG>::MAX_THREADS, MmaCfg<D, NHG>::M
 
   if (warp == C::NCW) {  // ---- producer warp
     if (lane == 0)
-      produce_tma<C>(&tmK, &tmV, stages, full, empty, ntiles, g,
-                     s * static_cast<int>(p.cache_cap) + c0, p.err);
+      produce_tma<C>(
+          &tmK, &tmV, stages, full, empty, ntiles, g,
+          [&](int i) {
+            return s * static_cast<int>(p.cache_cap) +
+                   (WIN ? tiles.start(c0 + i) : c0 + i * C::TP);
+          },
+          p.err);
     __syncwarp();
     if (clus) {
       cluster_sync();
@@ -208,10 +217,11 @@ __global__ void __launch_bounds__(MmaCfg<D, NHG>::MAX_THREADS, MmaCfg<D, NHG>::M
     if (!ok) break;
     const uint32_t sk = smem_addr(stages + st * C::STAGE_BYTES);
     const uint32_t sv = sk + C::NBOX * C::BOX_BYTES;
+    const int left = WIN ? tiles.end(c0 + i) - tiles.start(c0 + i) : c1 - (c0 + i * C::TP);
 #pragma unroll
     for (int b = 0; b < C::NB16; ++b) {
       const int r0 = slice * C::TPW + b * 16;
-      const int nv = min(max(c1 - (c0 + i * C::TP + r0), 0), 16);  // valid rows, a prefix
+      const int nv = min(max(left - r0, 0), 16);  // valid rows, a prefix
       if (nv == 0) continue;
       // -- S = Q . K^T for 16 positions (two n-tiles of 8)
       // four independent accumulator chains (n-tile x k-step parity), summed after
@@ -361,11 +371,11 @@ __global__ void __launch_bounds__(MmaCfg<D, NHG>::MAX_THREADS, MmaCfg<D, NHG>::M
 // (p.cluster != 0: a split grid that fits the GPU) and a row's chunks fit one cluster (2 .. 8),
 // the chunk CTAs of a row go out as one thread-block cluster and merge in distributed shared
 // memory instead of through the workspace.
-template <int D, int NHG>
+template <int D, int NHG, bool WIN = false>
 cudaError_t launch_mma_f16(const CUtensorMap& tk, const CUtensorMap& tv, PartialParams p,
                            dim3 grid, cudaStream_t s) {
   using C = MmaCfg<D, NHG>;
-  auto kern = &partial_mma_kernel<D, NHG>;
+  auto kern = &partial_mma_kernel<D, NHG, WIN>;
   const void* fn = reinterpret_cast<const void*>(kern);
   cudaError_t e = ensure_smem(fn, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;

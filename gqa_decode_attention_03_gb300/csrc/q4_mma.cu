@@ -63,10 +63,10 @@ __device__ __forceinline__ uint32_t mul_h2(uint32_t a, __half2 s) {
 
 template <int D>
 __global__ void __launch_bounds__(32 * Q4Cfg<D>::NW, Q4Cfg<D>::MIN_CTAS)
-    q4_mma_kernel(const VisibleParams vp) {
+    q4_mma_kernel(const Q4Params qp) {
   using C = Q4Cfg<D>;
   extern __shared__ __align__(128) uint8_t smem[];
-  const PartialParams& p = vp.base;
+  const PartialParams& p = qp.base;
   const int c = blockIdx.x, t = blockIdx.z;
   const int kvh = blockIdx.y / p.head_split;
   const int G = p.group / p.head_split;  // query heads of this CTA (<= 8)
@@ -78,8 +78,8 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D>::NW, Q4Cfg<D>::MIN_CTAS)
 
   int s = 0;
   const int L = visible_row(p, t, c == 0 && blockIdx.y == 0 && threadIdx.x == 0, s);
-  const Visible vis(L, vp.window, vp.n_sink);
-  const VisibleTiles<C::TP> tiles(vis);
+  const Visible vis(L, p.window, p.n_sink);
+  const VisibleTiles<C::TP, 16> tiles(vis);
   const int nchunks = (tiles.n + p.chunk - 1) / p.chunk;  // p.chunk: tiles of a chunk
   if (c >= nchunks) {
     if (c == 0)  // nothing to see: zeros
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D>::NW, Q4Cfg<D>::MIN_CTAS)
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     const uint32_t e = min(max(__float_as_uint(amax) >> 23, 1u), 253u);
     const float f = __uint_as_float((254u - e) << 23);  // 2^(127 - e)
-    sm = p.scale_log2 * vp.k_scale * __uint_as_float(e << 23);
+    sm = p.scale_log2 * qp.k_scale * __uint_as_float(e << 23);
 #pragma unroll
     for (int ks = 0; ks < C::KS; ++ks) {
       uint32_t a[4];
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D>::NW, Q4Cfg<D>::MIN_CTAS)
       A = fmaf(r[d], e, A);
       Ls = fmaf(r[D + 1], e, Ls);
     }
-    A *= vp.v_scale;
+    A *= qp.v_scale;
     const int head = head0 + h;
     if (split) {
       float* pr = p.part + (((size_t)t * p.n_split + c) * p.n_heads + head) * (D + 2);
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D>::NW, Q4Cfg<D>::MIN_CTAS)
 }
 
 template <int D>
-static cudaError_t launch_q4_d(const VisibleParams& vp, dim3 grid, cudaStream_t s) {
+static cudaError_t launch_q4_d(const Q4Params& qp, dim3 grid, cudaStream_t s) {
   using C = Q4Cfg<D>;
   const void* fn = reinterpret_cast<const void*>(&q4_mma_kernel<D>);
   cudaError_t e = ensure_smem(fn, C::SMEM);
@@ -403,14 +403,13 @@ static cudaError_t launch_q4_d(const VisibleParams& vp, dim3 grid, cudaStream_t 
   cudaLaunchAttribute at[2];
   cfg.attrs = at;
   cfg.numAttrs = cluster_attrs(at, 0, 1);
-  return cudaLaunchKernelEx(&cfg, &q4_mma_kernel<D>, vp);
+  return cudaLaunchKernelEx(&cfg, &q4_mma_kernel<D>, qp);
 }
 
-cudaError_t launch_q4(int head_dim, const VisibleParams& vp, const gqa_plan& plan, cudaStream_t s) {
-  const dim3 grid(plan.grid_x, plan.grid_y, plan.grid_z);
-  if (head_dim == 64) return launch_q4_d<64>(vp, grid, s);
-  if (head_dim == 128) return launch_q4_d<128>(vp, grid, s);
-  return launch_q4_d<256>(vp, grid, s);
+cudaError_t launch_q4(int head_dim, const Q4Params& qp, dim3 grid, cudaStream_t s) {
+  if (head_dim == 64) return launch_q4_d<64>(qp, grid, s);
+  if (head_dim == 128) return launch_q4_d<128>(qp, grid, s);
+  return launch_q4_d<256>(qp, grid, s);
 }
 
 }  // namespace gqa

@@ -16,13 +16,14 @@ struct Visible {
 };
 
 // Those positions as tiles of TP: first the sinks' from position 0, then the window's from w0
-// rounded down to 16.  Tile i holds positions [start, start + TP), of which [lo, end) are seen.
-template <int TP>
+// rounded down to a multiple of AL (a power of two).  Tile i holds positions [start, start + TP),
+// of which [lo, end) are seen.
+template <int TP, int AL>
 struct VisibleTiles {
   Visible v;
   int base, na, n;
   __host__ __device__ explicit VisibleTiles(const Visible& vis) : v(vis) {
-    base = v.w0 & ~15;
+    base = v.w0 & ~(AL - 1);
     na = (v.ns + TP - 1) / TP;
     n = na + (v.L - base + TP - 1) / TP;
   }
@@ -31,11 +32,11 @@ struct VisibleTiles {
   __host__ __device__ int end(int i) const { return i < na ? v.ns : v.L; }
 };
 
-struct VisibleParams {
-  PartialParams base;  // kc, vc, ksc, vsc hold the cache's pointers whatever its kind; chunk counts
-                       // tiles, n_valid is not used
-  int window, n_sink;
-  float k_scale, v_scale;  // 4-bit caches
+// The 4-bit kernel's arguments: base.kc, vc, ksc, vsc hold the cache's pointers, base.window and
+// n_sink what a row sees, base.chunk counts tiles.
+struct Q4Params {
+  PartialParams base;
+  float k_scale, v_scale;
 };
 
 constexpr int kQ4Tile = 32;  // positions of a tile of the 4-bit kernel

@@ -5,8 +5,8 @@
 
 namespace gqa {
 
-cudaError_t launch_q4(int head_dim, const VisibleParams& vp, const gqa_plan& plan, cudaStream_t s);
-cudaError_t launch_f16_window(int head_dim, const VisibleParams& vp, const gqa_plan& plan,
-                              cudaStream_t s);
+cudaError_t launch_q4(int head_dim, const Q4Params& qp, dim3 grid, cudaStream_t s);
+cudaError_t launch_f16_window(int head_dim, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const PartialParams& p, dim3 grid, cudaStream_t s);
 
 }  // namespace gqa

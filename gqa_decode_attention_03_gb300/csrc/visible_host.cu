@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdlib>
 
+#include "dispatch.h"
 #include "host_util.h"
 #include "visible_dispatch.h"
 
@@ -12,49 +13,52 @@ namespace gqa {
 
 bool q4_scale_ok(float s);  // append_q4.cu
 
-// 4-bit caches: chunks of whole tiles, so many that about kQ4Waves CTAs per resident slot share
-// the rows at their longest, none shorter than two tiles a warp.
+// Chunks of whole tiles, as many as fill the CTA slots of the GPU once at the rows' longest, within
+// these bounds.
 constexpr int kQ4CtasPerSm = 3;
-constexpr int kQ4MaxChunkTiles = 64;
-constexpr int kQ4MinChunkTiles = 8;
+constexpr int kQ4MaxChunk = 2048, kQ4MinChunk = 256;
+constexpr int kWinCtasPerSm = 2;
+constexpr int kWinMaxChunk = 4096, kWinMinStages = 2;
 
 gqa_status plan_visible(int n_tok, int n_seq, int n_heads, int n_kv_heads, int head_dim,
                         int max_kv_len, int budget, int kind, int num_sms, gqa_plan* plan) {
   (void)n_seq;
   if (budget == 0 || budget < -1)
     return fail(GQA_EINVAL, "budget %d: window + n_sink, or -1 for every position", budget);
-  const int n = budget > 0 ? std::min(max_kv_len, budget) : max_kv_len;
-  if (kind == GQA_KIND_F16_WINDOW) {
-    plan->chunk = std::max(n, 1);
-    plan->n_split = 1;
-    plan->tile = 1;
-    plan->grid_x = n_heads;
-    plan->grid_y = n_tok;
-    plan->grid_z = 1;
-    return GQA_OK;
-  }
+  const long long n = budget > 0 ? std::min(max_kv_len, budget) : max_kv_len;
   if (num_sms <= 0) {
     gqa_status st = GQA_OK;
     num_sms = current_sm_count(&st);
     if (num_sms <= 0) return st != GQA_OK ? st : fail(GQA_ECUDA, "no SM count");
   }
+  const bool q4 = kind == GQA_KIND_Q4;
   const int group = n_heads / n_kv_heads;
-  int hs = 1;  // CTAs of a KV head's query heads, at most 8 each
-  while (group % hs || group / hs > 8) ++hs;
-  // the sinks' last tile and the window's first one may be partly seen
-  const long long tiles = ((long long)n + kQ4Tile - 1) / kQ4Tile + (budget > 0 ? 2 : 0);
-  const long long units = (long long)n_tok * n_kv_heads * hs;
-  const long long slots = (long long)kQ4CtasPerSm * num_sms;
-  long long chunk = (std::max(units, 1LL) * tiles + slots - 1) / slots;
-  chunk = std::min<long long>(std::max<long long>(chunk, kQ4MinChunkTiles), kQ4MaxChunkTiles);
-  if (const char* f = std::getenv("GQA_FORCE_CHUNK"))
-    if (std::atoi(f) > 0) chunk = (std::atoi(f) + kQ4Tile - 1) / kQ4Tile;
+  int hs = 1;  // 4-bit: CTAs of a KV head's query heads, at most 8 each
+  while (q4 && (group % hs || group / hs > 8)) ++hs;
+  const int tile = q4 ? kQ4Tile : stage_rows(GQA_KIND_F16, head_dim);
+  // the sinks' last tile and the window's last one (4-bit: its first one too) are partly seen
+  const long long tiles = (n + tile - 1) / tile + (budget > 0 ? 2 : 0);
+  const long long units = std::max(1LL, (long long)n_tok * n_kv_heads * hs);
+  const long long slots = (long long)(q4 ? kQ4CtasPerSm : kWinCtasPerSm) * num_sms;
+  long long chunk = (units * tiles + slots - 1) / slots;
+  chunk = std::max<long long>(chunk, q4 ? kQ4MinChunk / tile : kWinMinStages);
+  chunk = std::min<long long>(chunk, (q4 ? kQ4MaxChunk : kWinMaxChunk) / tile);
+  const char* f = std::getenv("GQA_FORCE_CHUNK");
+  const int forced = f ? std::atoi(f) : 0;
+  if (forced > 0) {
+    chunk = (forced + tile - 1) / tile;
+  } else if (!q4 && chunk < tiles) {
+    // a split grid that fits the GPU merges each row in a cluster of up to 8 chunk CTAs
+    const long long c8 = (tiles + 7) / 8;
+    if (units * ((tiles + c8 - 1) / c8) <= num_sms) chunk = c8;
+  }
+  chunk = std::min(chunk, std::max(tiles, 1LL));
   const long long n_split = std::max(1LL, (tiles + chunk - 1) / chunk);
   if (n_split > (1 << 30) || (long long)n_kv_heads * hs > 65535)
     return fail(GQA_EUNSUPPORTED, "too many chunks or heads for one launch");
-  plan->chunk = (int)(chunk * kQ4Tile);
+  plan->chunk = (int)std::min<long long>(chunk * tile, INT_MAX / tile * tile);
   plan->n_split = (int)n_split;
-  plan->tile = kQ4Tile;
+  plan->tile = tile;
   plan->grid_x = (int)n_split;
   plan->grid_y = n_kv_heads * hs;
   plan->grid_z = n_tok;
@@ -111,8 +115,8 @@ static gqa_status visible_common(int kind, const float* q, const void* kc, const
     return fail(GQA_EWORKSPACE, "workspace needs %zu bytes (16-byte aligned), got %zu",
                 plan.ws_bytes, ws ? ws_bytes : (size_t)0);
 
-  VisibleParams vp{};
-  PartialParams& p = vp.base;
+  Q4Params qp{};
+  PartialParams& p = qp.base;
   p.q = q;
   p.kc = kc;
   p.vc = vc;
@@ -141,12 +145,24 @@ static gqa_status visible_common(int kind, const float* q, const void* kc, const
   }
   p.gate = gate;
   p.gate_stride = gate ? gate_stride : 0;
-  vp.window = window;
-  vp.n_sink = n_sink;
-  vp.k_scale = k_scale;
-  vp.v_scale = v_scale;
-  const cudaError_t e = q4 ? launch_q4(head_dim, vp, plan, stream)
-                           : launch_f16_window(head_dim, vp, plan, stream);
+  p.window = window;
+  p.n_sink = n_sink;
+  p.pdl = 1;
+  const dim3 grid(plan.grid_x, plan.grid_y, plan.grid_z);
+  cudaError_t e;
+  if (q4) {
+    qp.k_scale = k_scale;
+    qp.v_scale = v_scale;
+    e = launch_q4(head_dim, qp, grid, stream);
+  } else {
+    CUtensorMap tk, tv;
+    st = encode_f16_cache(kc, vc, n_seq, cache_cap, n_kv_heads, head_dim, plan.tile, &tk, &tv);
+    if (st != GQA_OK) return st;
+    st = GQA_OK;
+    p.cluster = plan.merge && (long long)plan.grid_x * plan.grid_y * plan.grid_z <=
+                                  current_sm_count(&st);
+    e = launch_f16_window(head_dim, tk, tv, p, grid, stream);
+  }
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return cuda_fail(e, q4 ? "attn_decode_q4 launch" : "attn_decode_f16_window launch");

@@ -417,7 +417,8 @@ gqa_status kv_read_q4(const uint8_t* kq, const uint8_t* vq, const uint8_t* ksc,
  *   j >= kv_len[t] - window   (the last `window` positions), or
  *   j < n_sink                (the first positions, which stay visible),
  * each once.  window 0 means no window (every position; attn_decode_q4 only).  Nothing outside
- * that set reaches the output.
+ * that set reaches the output, NaN and infinities included.  An infinity or NaN in an f16 V row
+ * that a row does see leaves the dim without a finite value (an infinity may come out as NaN).
  *
  * attn_decode_q4 -- decode attention over a 4-bit cache (layout above), dense or windowed.
  *   window        >= 0; n_sink >= 0 (not used with window 0)
