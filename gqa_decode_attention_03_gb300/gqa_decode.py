@@ -392,35 +392,52 @@ def kv_append_q8(k_new, v_new, kq, vq, ksc, vsc, seq, t0, stream=None):
                                int(t0), _stream(stream)))
 
 
-def _need_all(device, *specs):
-    """``_need`` over (tensor, dtype, name, ndim), and all on the current CUDA device."""
-    for x, dtype, name, ndim in specs:
-        _need(x, dtype, name, ndim)
-        if x.get_device() != device:
-            raise ValueError(f"{name} is on cuda:{x.get_device()}, the current device is "
-                             f"cuda:{device}")
+# The checks of the calls below.  A decode step's launch takes ~3 us on the host, so a call that is
+# in order is told by one look at each tensor (``_off``); only one that is not goes through the
+# checks that name the argument.
+
+def _off(x, dtype, device):
+    """Whether x is anything but a contiguous tensor of this type on this CUDA device."""
+    try:
+        return x.dtype is not dtype or x.get_device() != device or not x.is_contiguous()
+    except AttributeError:
+        return True
+
+
+def _refuse(x, dtype, name, device, ndim=None):
+    """Raises for an argument that ``_off`` or its shape has turned down."""
+    _need(x, dtype, name, ndim)
+    if x.get_device() != device:
+        raise ValueError(f"{name} is on cuda:{x.get_device()}, the current device is cuda:{device}")
 
 
 def _need_err(err, device):
-    if err is not None:
-        _need_all(device, (err, torch.int32, "err", None))
-        if err.numel() < 1:
-            raise ValueError("err must hold one int32")
+    if _off(err, torch.int32, device):
+        _refuse(err, torch.int32, "err", device)
+    if err.numel() < 1:
+        raise ValueError("err must hold one int32")
 
 
 def _q4_cache(kq, vq, ksc, vsc, device):
     """(n_seq, Hk, cap, D) of a 4-bit cache, checked."""
-    _need_all(device, (kq, torch.uint8, "kq", 4), (vq, torch.uint8, "vq", 4),
-              (ksc, torch.uint8, "ksc", 4), (vsc, torch.uint8, "vsc", 4))
-    n_seq, Hk, cap, D2 = kq.shape
-    if vq.shape != kq.shape or vsc.shape != ksc.shape or ksc.shape != (n_seq, Hk, cap, D2 // 8):
+    u8 = torch.uint8
+    if _off(kq, u8, device) or _off(vq, u8, device) or _off(ksc, u8, device) or _off(vsc, u8, device):
+        for x, name in ((kq, "kq"), (vq, "vq"), (ksc, "ksc"), (vsc, "vsc")):
+            _refuse(x, u8, name, device)
+    shape, scales = kq.shape, ksc.shape
+    if len(shape) != 4:
+        raise ValueError(f"kq must have 4 dims, got {len(shape)}")
+    n_seq, Hk, cap, D2 = shape
+    if vq.shape != shape or vsc.shape != scales or scales != (n_seq, Hk, cap, D2 // 8):
         raise ValueError("shape mismatch between the 4-bit cache's codes and scales")
     return n_seq, Hk, cap, 2 * D2
 
 
 def _ragged(row_off, t0, n_seq, device):
-    _need_all(device, (row_off, torch.int32, "row_off", 1), (t0, torch.int32, "t0", 1))
-    if row_off.numel() != n_seq + 1 or t0.numel() != n_seq:
+    if _off(row_off, torch.int32, device) or _off(t0, torch.int32, device):
+        _refuse(row_off, torch.int32, "row_off", device, 1)
+        _refuse(t0, torch.int32, "t0", device, 1)
+    if row_off.shape != (n_seq + 1,) or t0.shape != (n_seq,):
         raise ValueError("row_off must hold n_seq + 1 entries and t0 n_seq")
 
 
@@ -436,25 +453,31 @@ def kv_append_q4(k_new, v_new, kq, vq, ksc, vsc, row_off, t0, k_scale=1.0, v_sca
     """
     device = _current_device()
     n_seq, Hk, cap, D = _q4_cache(kq, vq, ksc, vsc, device)
-    _need_all(device, (k_new, torch.float32, "k_new", 3), (v_new, torch.float32, "v_new", 3))
     _ragged(row_off, t0, n_seq, device)
-    _need_err(err, device)
-    n = k_new.shape[0]
-    if k_new.shape != (n, Hk, D) or v_new.shape != (n, Hk, D):
+    if _off(k_new, torch.float32, device) or _off(v_new, torch.float32, device):
+        _refuse(k_new, torch.float32, "k_new", device)
+        _refuse(v_new, torch.float32, "v_new", device)
+    if err is not None:
+        _need_err(err, device)
+    shape = k_new.shape
+    if len(shape) != 3 or shape[1:] != (Hk, D) or v_new.shape != shape:
         raise ValueError("shape mismatch between new rows and the cache")
-    _check(LIB.kv_append_q4(_ptr(k_new), _ptr(v_new), n, Hk, D, _ptr(row_off), _ptr(t0),
-                            float(k_scale), float(v_scale), _ptr(kq), _ptr(vq), _ptr(ksc),
-                            _ptr(vsc), n_seq, cap, _ptr(err), _stream(stream)))
+    _check(LIB.kv_append_q4(k_new.data_ptr(), v_new.data_ptr(), shape[0], Hk, D,
+                            row_off.data_ptr(), t0.data_ptr(), k_scale, v_scale, kq.data_ptr(),
+                            vq.data_ptr(), ksc.data_ptr(), vsc.data_ptr(), n_seq, cap, _ptr(err),
+                            _stream(stream)))
 
 
 def kv_read_q4(kq, vq, ksc, vsc, row_off, t0, k_out=None, v_out=None, n_rows=None, k_scale=1.0,
                v_scale=1.0, dtype=torch.float32, err=None, stream=None):
     """The values of rows of the 4-bit cache: (k, v) [n_rows][Hk][D] in fp32 or fp16, the rows
-    addressed as in ``kv_append_q4``.  Give k_out and v_out, or n_rows (and dtype) for new ones."""
+    addressed as in ``kv_append_q4``.  Give k_out and v_out, or n_rows (and dtype) for new ones
+    (zeros where no sequence holds the row)."""
     device = _current_device()
     n_seq, Hk, cap, D = _q4_cache(kq, vq, ksc, vsc, device)
     _ragged(row_off, t0, n_seq, device)
-    _need_err(err, device)
+    if err is not None:
+        _need_err(err, device)
     if (k_out is None) != (v_out is None):
         raise ValueError("give both k_out and v_out, or neither")
     if k_out is None:
@@ -466,52 +489,65 @@ def kv_read_q4(kq, vq, ksc, vsc, row_off, t0, k_out=None, v_out=None, n_rows=Non
         raise TypeError("k_out must be a torch.Tensor")
     else:
         dtype = k_out.dtype
-    if dtype not in (torch.float32, torch.float16):
+    half = dtype is torch.float16
+    if not half and dtype is not torch.float32:
         raise TypeError(f"rows are read as float32 or float16, not {dtype}")
-    _need_all(device, (k_out, dtype, "k_out", 3), (v_out, dtype, "v_out", 3))
-    n = k_out.shape[0]
-    if k_out.shape != (n, Hk, D) or v_out.shape != (n, Hk, D) or n_rows not in (None, n):
+    if _off(k_out, dtype, device) or _off(v_out, dtype, device):
+        _refuse(k_out, dtype, "k_out", device)
+        _refuse(v_out, dtype, "v_out", device)
+    shape = k_out.shape
+    if (len(shape) != 3 or shape[1:] != (Hk, D) or v_out.shape != shape
+            or n_rows not in (None, shape[0])):
         raise ValueError("shape mismatch between the output rows and the cache")
-    _check(LIB.kv_read_q4(_ptr(kq), _ptr(vq), _ptr(ksc), _ptr(vsc), n_seq, cap, n, Hk, D,
-                          _ptr(row_off), _ptr(t0), float(k_scale), float(v_scale), _ptr(k_out),
-                          _ptr(v_out), 1 if dtype == torch.float16 else 0, _ptr(err),
-                          _stream(stream)))
+    if v_out.data_ptr() == k_out.data_ptr() and shape[0]:
+        raise ValueError("v_out must not be k_out")
+    _check(LIB.kv_read_q4(kq.data_ptr(), vq.data_ptr(), ksc.data_ptr(), vsc.data_ptr(), n_seq, cap,
+                          shape[0], Hk, D, row_off.data_ptr(), t0.data_ptr(), k_scale, v_scale,
+                          k_out.data_ptr(), v_out.data_ptr(), half, _ptr(err), _stream(stream)))
     return k_out, v_out
 
 
-def _visible_args(q, kv_len, seq_of, n_seq, Hk, cap, Dk, scale, max_kv_len, window, n_sink, out,
-                  ws, err, gate, gate_stride, kind, device):
-    """The arguments that the calls with a visible set share, checked: (T, H, D, scale,
-    max_kv_len, window, n_sink, out, ws, gate_stride)."""
-    _need_all(device, (q, torch.float32, "q", 3), (kv_len, torch.int32, "kv_len", 1))
-    if seq_of is not None:
-        _need_all(device, (seq_of, torch.int32, "seq_of", 1))
-    T, H, D = q.shape
-    if Dk != D or kv_len.numel() != T or (seq_of is not None and seq_of.numel() != T):
+def _visible_args(q, kv_len, seq_of, n_seq, Hk, cap, Dk, max_kv_len, window, n_sink, out, ws, err,
+                  kind, device):
+    """The arguments that the calls with a visible set share, checked: (T, H, max_kv_len, out, ws)."""
+    if _off(q, torch.float32, device) or _off(kv_len, torch.int32, device):
+        _refuse(q, torch.float32, "q", device)
+        _refuse(kv_len, torch.int32, "kv_len", device)
+    if seq_of is not None and _off(seq_of, torch.int32, device):
+        _refuse(seq_of, torch.int32, "seq_of", device)
+    shape = q.shape
+    if len(shape) != 3:
+        raise ValueError(f"q must have 3 dims, got {len(shape)}")
+    T, H, D = shape
+    if (Dk != D or kv_len.shape != (T,) or (seq_of is not None and seq_of.shape != (T,))):
         raise ValueError("shape mismatch between q, caches, kv_len and seq_of")
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     max_kv_len = cap if max_kv_len is None else int(max_kv_len)
-    window, n_sink = int(window or 0), int(n_sink)
     if not (0 <= window < 1 << 31 and 0 <= n_sink < 1 << 31 and max_kv_len < 1 << 31):
         raise ValueError("window, n_sink and max_kv_len must lie in [0, 2^31)")
     if out is None:
         out = torch.empty_like(q)
-    _need_all(device, (out, torch.float32, "out", 3))
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    if T and out.data_ptr() == q.data_ptr():
-        raise ValueError("out must not be q")
+    else:
+        if _off(out, torch.float32, device):
+            _refuse(out, torch.float32, "out", device)
+        if out.shape != shape:
+            raise ValueError("out must have q's shape")
+        if T and out.data_ptr() == q.data_ptr():
+            raise ValueError("out must not be q")
     if ws is None:
         budget = min(window + n_sink, (1 << 31) - 1) if window else -1
         ws = alloc_workspace(T, H, Hk, D, min(max_kv_len, cap), budget, kind, q.device, n_seq)
-    elif not (ws.is_cuda and ws.is_contiguous() and ws.get_device() == device):
+    elif ws.get_device() != device or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous tensor on the current CUDA device")
-    _need_err(err, device)
-    gs = 0
-    if gate is not None:
-        gs = _gate_args(gate, gate_stride, T, H, D)
-        _need_all(device, (gate, torch.float32, "gate", None))
-    return T, H, D, scale, max_kv_len, window, n_sink, out, ws, gs
+    if err is not None:
+        _need_err(err, device)
+    return T, H, max_kv_len, out, ws
+
+
+def _visible_gate(gate, gate_stride, T, H, D, device):
+    gs = _gate_args(gate, gate_stride, T, H, D)
+    if _off(gate, torch.float32, device):
+        _refuse(gate, torch.float32, "gate", device)
+    return gs
 
 
 def attn_decode_q4(q, kq, vq, ksc, vsc, kv_len, scale=None, k_scale=1.0, v_scale=1.0, window=None,
@@ -524,15 +560,17 @@ def attn_decode_q4(q, kq, vq, ksc, vsc, kv_len, scale=None, k_scale=1.0, v_scale
     fp32 sigmoid output gate, see ``_gate_args``.
     """
     device = _current_device()
-    n_seq, Hk, cap, Dk = _q4_cache(kq, vq, ksc, vsc, device)
-    T, H, D, scale, max_kv_len, window, n_sink, out, ws, gs = _visible_args(
-        q, kv_len, seq_of, n_seq, Hk, cap, Dk, scale, max_kv_len, window,
-        n_sink if window else 0, out, ws, err, gate, gate_stride, KIND_Q4, device)
-    _check(LIB.attn_decode_q4(_ptr(q), _ptr(kq), _ptr(vq), _ptr(ksc), _ptr(vsc), float(k_scale),
-                              float(v_scale), window, n_sink, _ptr(out), _ptr(kv_len),
-                              _ptr(seq_of), T, n_seq, H, Hk, D, cap, max_kv_len, scale, _ptr(gate),
-                              gs, _ptr(ws), ws.numel() * ws.element_size(), _ptr(err),
-                              _stream(stream)))
+    n_seq, Hk, cap, D = _q4_cache(kq, vq, ksc, vsc, device)
+    window = 0 if window is None else int(window)
+    n_sink = int(n_sink) if window else 0
+    T, H, max_kv_len, out, ws = _visible_args(q, kv_len, seq_of, n_seq, Hk, cap, D, max_kv_len,
+                                              window, n_sink, out, ws, err, KIND_Q4, device)
+    gs = 0 if gate is None else _visible_gate(gate, gate_stride, T, H, D, device)
+    _check(LIB.attn_decode_q4(q.data_ptr(), kq.data_ptr(), vq.data_ptr(), ksc.data_ptr(),
+                              vsc.data_ptr(), k_scale, v_scale, window, n_sink, out.data_ptr(),
+                              kv_len.data_ptr(), _ptr(seq_of), T, n_seq, H, Hk, D, cap, max_kv_len,
+                              1.0 / math.sqrt(D) if scale is None else scale, _ptr(gate), gs,
+                              ws.data_ptr(), ws.nbytes, _ptr(err), _stream(stream)))
     return out
 
 
@@ -542,20 +580,25 @@ def attn_decode_f16_window(q, k_cache, v_cache, kv_len, window, n_sink=0, scale=
     """``attn_decode_f16`` through a sliding window: row t sees its last `window` positions and the
     first n_sink.  Rows that share a sequence (a prefill chunk) each have their own window."""
     device = _current_device()
-    _need_all(device, (k_cache, torch.float16, "k_cache", 4),
-              (v_cache, torch.float16, "v_cache", 4))
-    if k_cache.shape != v_cache.shape:
-        raise ValueError("k_cache and v_cache shapes differ")
-    if not window or int(window) < 1:
+    if _off(k_cache, torch.float16, device) or _off(v_cache, torch.float16, device):
+        _refuse(k_cache, torch.float16, "k_cache", device)
+        _refuse(v_cache, torch.float16, "v_cache", device)
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must have the same 4 dims")
+    window = 0 if window is None else int(window)
+    if window < 1:
         raise ValueError("window must be >= 1")
-    n_seq, cap, Hk, Dk = k_cache.shape
-    T, H, D, scale, max_kv_len, window, n_sink, out, ws, gs = _visible_args(
-        q, kv_len, seq_of, n_seq, Hk, cap, Dk, scale, max_kv_len, window, n_sink, out, ws, err,
-        gate, gate_stride, KIND_F16_WINDOW, device)
-    _check(LIB.attn_decode_f16_window(_ptr(q), _ptr(k_cache), _ptr(v_cache), window, n_sink,
-                                      _ptr(out), _ptr(kv_len), _ptr(seq_of), T, n_seq, H, Hk, D,
-                                      cap, max_kv_len, scale, _ptr(gate), gs, _ptr(ws),
-                                      ws.numel() * ws.element_size(), _ptr(err), _stream(stream)))
+    n_sink = int(n_sink)
+    n_seq, cap, Hk, D = shape
+    T, H, max_kv_len, out, ws = _visible_args(q, kv_len, seq_of, n_seq, Hk, cap, D, max_kv_len,
+                                              window, n_sink, out, ws, err, KIND_F16_WINDOW, device)
+    gs = 0 if gate is None else _visible_gate(gate, gate_stride, T, H, D, device)
+    _check(LIB.attn_decode_f16_window(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), window,
+                                      n_sink, out.data_ptr(), kv_len.data_ptr(), _ptr(seq_of), T,
+                                      n_seq, H, Hk, D, cap, max_kv_len,
+                                      1.0 / math.sqrt(D) if scale is None else scale, _ptr(gate),
+                                      gs, ws.data_ptr(), ws.nbytes, _ptr(err), _stream(stream)))
     return out
 
 
