@@ -308,6 +308,7 @@ __global__ void __launch_bounds__(MmaCfg<D, NHG>::MAX_THREADS, MmaCfg<D, NHG>::M
   // ---- per-thread l covers its own positions: sum the quad
   l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
   l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
+  if constexpr (WIN) keep_nan(m_run, l_run, o);
 
   // ---- merge the row slices (log-sum-exp) and write
   named_bar_sync(1, C::NCW * 32);

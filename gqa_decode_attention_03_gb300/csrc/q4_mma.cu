@@ -344,6 +344,7 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D>::NW, Q4Cfg<D>::MIN_CTAS)
   }
   l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
   l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
+  keep_nan(m_run, l_run, o);
 
   // ---- the four warps' states meet in shared memory (over the rings, which are drained)
   __syncthreads();

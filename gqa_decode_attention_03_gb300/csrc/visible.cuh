@@ -39,7 +39,8 @@ struct Q4Params {
   float k_scale, v_scale;
 };
 
-constexpr int kQ4Tile = 32;  // positions of a tile of the 4-bit kernel
+constexpr int kQ4Tile = 32;        // positions of a tile of the 4-bit kernel
+constexpr int kWinRowsTile = 128;  // ... of the kernel for rows that share a sequence
 
 // Row t's length and sequence; values out of range are flagged (by the thread that `flag` names)
 // and clamped, a row of a bad sequence sees nothing.
@@ -56,6 +57,21 @@ __device__ __forceinline__ int visible_row(const PartialParams& p, int t, bool f
   }
   if (errbits && flag) flag_error(p.err, errbits);
   return L;
+}
+
+// A sum that is NaN (a NaN or infinite score in sight) has to outlast the merges, which take a row
+// without a positive sum for one that sees nothing.  Its state becomes a maximum above every other
+// (log2 units), an infinite sum and a NaN accumulator: the merged row is NaN / infinity.
+constexpr float kNanMax = 1e30f;
+template <int N, int K>
+__device__ __forceinline__ void keep_nan(float& m, float& l, float (&o)[N][K]) {
+  if (l == l) return;
+  m = kNanMax;
+  l = INFINITY;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int k = 0; k < K; ++k) o[n][k] = __int_as_float(0x7fffffff);
 }
 
 }  // namespace gqa

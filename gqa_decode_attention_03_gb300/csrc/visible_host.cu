@@ -4,6 +4,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdlib>
+#include <cstring>
 
 #include "dispatch.h"
 #include "host_util.h"
@@ -19,10 +20,18 @@ constexpr int kQ4CtasPerSm = 3;
 constexpr int kQ4MaxChunk = 2048, kQ4MinChunk = 256;
 constexpr int kWinCtasPerSm = 2;
 constexpr int kWinMaxChunk = 4096, kWinMinStages = 2;
+constexpr int kWinRowsMinPairs = 32;
+
+// Rows that share a sequence go to the kernel that serves 128 (row, head) pairs a CTA when there
+// are enough of them.
+static bool window_rows_grouped(int n_tok, int n_seq, int group, int head_dim) {
+  const char* r = std::getenv("GQA_F16_ROWS");  // "off": one CTA per row (tests, comparison)
+  if (r && std::strcmp(r, "off") == 0) return false;
+  return head_dim != 256 && (long long)n_tok * group >= (long long)kWinRowsMinPairs * n_seq;
+}
 
 gqa_status plan_visible(int n_tok, int n_seq, int n_heads, int n_kv_heads, int head_dim,
                         int max_kv_len, int budget, int kind, int num_sms, gqa_plan* plan) {
-  (void)n_seq;
   if (budget == 0 || budget < -1)
     return fail(GQA_EINVAL, "budget %d: window + n_sink, or -1 for every position", budget);
   const long long n = budget > 0 ? std::min(max_kv_len, budget) : max_kv_len;
@@ -33,6 +42,27 @@ gqa_status plan_visible(int n_tok, int n_seq, int n_heads, int n_kv_heads, int h
   }
   const bool q4 = kind == GQA_KIND_Q4;
   const int group = n_heads / n_kv_heads;
+  if (!q4 && window_rows_grouped(n_tok, n_seq, group, head_dim)) {
+    const int r = 128 / group;
+    const long long groups = (n_tok + r - 1) / r;
+    const long long most = std::max(1LL, (n + kWinRowsTile - 1) / kWinRowsTile);
+    // one CTA per SM; a grid that leaves half of the SMs idle is split over the positions
+    const long long n_split =
+        std::max(1LL, std::min(num_sms / std::max(1LL, groups * n_kv_heads), most));
+    plan->n_split = (int)n_split;
+    plan->tile = kWinRowsTile;
+    plan->chunk = (int)((most + n_split - 1) / n_split * kWinRowsTile);
+    plan->grid_x = (int)n_split;
+    plan->grid_y = n_kv_heads;
+    plan->grid_z = (int)groups;
+    plan->row_group = r;
+    plan->merge = n_split > 1 ? 1 : 0;
+    if (plan->merge) {
+      const size_t part = (size_t)n_tok * n_split * n_heads * (head_dim + 2) * sizeof(float);
+      plan->ws_bytes = (part + 255) / 256 * 256 + (size_t)n_tok * sizeof(int32_t);
+    }
+    return GQA_OK;
+  }
   int hs = 1;  // 4-bit: CTAs of a KV head's query heads, at most 8 each
   while (q4 && (group % hs || group / hs > 8)) ++hs;
   const int tile = q4 ? kQ4Tile : stage_rows(GQA_KIND_F16, head_dim);
@@ -138,7 +168,11 @@ static gqa_status visible_common(int kind, const float* q, const void* kc, const
   p.scale_log2 = scale * 1.4426950408889634f;
   p.merge = plan.merge;
   p.head_split = std::max(1, plan.grid_y / n_kv_heads);
-  if (plan.merge) {  // ws = [arrival counters][partials]
+  if (plan.merge && plan.row_group > 1) {  // ws = [partials][n_valid]
+    const size_t part = (size_t)n_tok * plan.n_split * n_heads * (head_dim + 2) * sizeof(float);
+    p.part = static_cast<float*>(ws);
+    p.n_valid = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + (part + 255) / 256 * 256);
+  } else if (plan.merge) {  // ws = [arrival counters][partials]
     const size_t cnt = ((size_t)n_tok * plan.grid_y * sizeof(uint32_t) + 255) / 256 * 256;
     p.counters = static_cast<unsigned int*>(ws);
     p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + cnt);
@@ -161,7 +195,11 @@ static gqa_status visible_common(int kind, const float* q, const void* kc, const
     st = GQA_OK;
     p.cluster = plan.merge && (long long)plan.grid_x * plan.grid_y * plan.grid_z <=
                                   current_sm_count(&st);
-    e = launch_f16_window(head_dim, tk, tv, p, grid, stream);
+    e = plan.row_group > 1 ? launch_window_rows(head_dim, tk, tv, p, grid, stream)
+                           : launch_f16_window(head_dim, tk, tv, p, grid, stream);
+    if (e == cudaSuccess && plan.row_group > 1 && plan.merge)
+      e = launch_merge(head_dim, p.part, p.n_valid, plan.n_split, n_tok, n_heads, out, stream,
+                       p.gate, p.gate_stride, /*after_partials=*/true);
   }
   if (e != cudaSuccess) {
     (void)cudaGetLastError();

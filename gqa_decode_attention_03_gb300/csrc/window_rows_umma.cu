@@ -1,0 +1,583 @@
+// window_rows_umma.cu -- windowed f16 attention of rows that share a sequence (a chunk of a prompt)
+// on the fifth-generation tensor cores.
+//
+// One CTA serves the 128 / G consecutive query rows of a group for one KV head: their (row, head)
+// pairs are the M = 128 rows of its MMAs, one softmax thread each, so every K/V tile is read once
+// for all of them.  Per tile of 128 positions
+//   S  = Q . K^T     fp32 in TMEM; Q (scale * log2 e folded in) as f16 hi + f16 lo, two MMAs a
+//                    k-step into the same S
+//   P  = 2^(S - m)   by the row's thread: masked by its own row's window, the running maximum
+//                    moves only when a tile exceeds it by 2^8; written back over S in TMEM as f16
+//                    hi and lo parts (64 columns each)
+//   O += P . V       fp32 in TMEM, A = P from TMEM, two MMAs a k-step
+// hi + lo keep ~22 bits of q and of the weights; K and V are f16 as they are.
+//
+// Three S/P buffers: the issuer's order S(j+1), PV(j) gives the softmax of tile j the time of
+// PV(j-1) and S(j+1), and no MMA waits for the one just before it.  The tiles of a group are those
+// of the union of its rows' visible positions, sequence by sequence where a group's rows belong to
+// several (consecutive rows of one sequence form a run; a row's weights are 0 outside its run).
+//
+// A hidden position weighs 0, but 0 times an infinity or NaN is NaN.  V rows that no row of the run
+// sees are zeroed in shared memory; in a tile that only some rows see whole, V is searched for such
+// values, and a group that meets one is computed again at the end without matrix products
+// (rows_plain), which skips hidden positions.
+#include "dispatch.h"
+#include "umma.cuh"
+#include "visible.cuh"
+#include "visible_dispatch.h"
+
+namespace gqa {
+
+template <int D>
+struct WinRowsCfg {
+  static constexpr int M = 128, TP = kWinRowsTile;
+  static constexpr int NBOX = D / 64;
+  static constexpr int BOX = TP * 128;             // a box: TP rows x 128 bytes
+  static constexpr int KT = NBOX * BOX;            // a K or V tile
+  static constexpr int NK = 2, NV = 2;             // ring slots
+  static constexpr int Q_BOX = M * 128, Q_PART = NBOX * Q_BOX;
+  static constexpr int NB = 3;                     // S/P buffers in TMEM
+  static constexpr int O_COL = NB * TP, TMEM_COLS = 512;
+  static constexpr int KS_S = D / 16, KS_O = TP / 16;
+  static constexpr int NSW = 4, PRODUCER = 4, ISSUER = 5, THREADS = 192;
+  static constexpr int Q_OFF = (NK + NV) * KT;
+  static constexpr int NBAR = 2 * NK + 2 * NV + 3 * NB + 2;
+  static constexpr int BAR_OFF = Q_OFF + 2 * Q_PART;
+  static constexpr int TAB_OFF = align_up(BAR_OFF + NBAR * 8 + 16, 16);
+  static constexpr int SMEM = 1024 + TAB_OFF;
+  static constexpr float RESCALE_LOG2 = 8.f;
+  static_assert(O_COL + D <= TMEM_COLS, "TMEM columns");
+  static_assert(TP == 128 && M == 128, "one P column pair per S column");
+};
+
+// A run of consecutive rows of one sequence: the union of what they see, as tiles.
+struct WinRun {
+  int seq, tiles0;               // sequence; index of its first tile in the group's list
+  int na, base;                  // tiles of the sinks; where the window tiles start
+  int ns, end;                   // union: [0, ns) (if na) and [base, end)
+  int ns_min, w0_max, end_min;   // what every row of the run sees: [0, ns_min), [w0_max, end_min)
+};
+
+struct WinRowsTable {
+  int len[128], seq[128];
+  int run[128];    // row -> its run, -1 for a row that sees nothing
+  WinRun runs[129];  // runs[nruns].tiles0: the number of tiles
+  int nruns, dirty;
+};
+
+struct WinTile {
+  int start, end, seq;  // positions [start, min(start + TP, end)) of a sequence
+};
+
+// The group's tile i; k: the run of an earlier tile, moved on to this one's.
+__device__ __forceinline__ WinTile win_tile(const WinRowsTable& tb, int i, int& k) {
+  while (i >= tb.runs[k + 1].tiles0) ++k;
+  const WinRun& r = tb.runs[k];
+  const int j = i - r.tiles0;
+  WinTile w;
+  w.seq = r.seq;
+  w.start = j < r.na ? j * kWinRowsTile : r.base + (j - r.na) * kWinRowsTile;
+  w.end = j < r.na ? r.ns : r.end;
+  return w;
+}
+
+// Thread-serial or warp-wide (one sequence) construction of the runs; warp 0.
+__device__ void win_build(WinRowsTable& tb, int nr, int window, int n_sink, int lane) {
+  auto finish = [](WinRun& r, int tiles0) {
+    r.tiles0 = tiles0;
+    if (r.base <= r.ns) r.base = r.ns = 0;  // the two parts meet: [0, end)
+    r.na = (r.ns + kWinRowsTile - 1) / kWinRowsTile;
+    return tiles0 + r.na + (r.end - r.base + kWinRowsTile - 1) / kWinRowsTile;
+  };
+  int first = -1;
+  bool same = true;
+  for (int j = 0; j < nr; j += 32) {
+    const bool on = j + lane < nr && tb.len[j + lane] > 0;
+    const unsigned b = __ballot_sync(0xffffffffu, on);
+    if (!b) continue;
+    if (first < 0) first = tb.seq[j + __ffs(b) - 1];
+    same = same && __all_sync(0xffffffffu, !on || tb.seq[j + lane] == first);
+  }
+  if (same) {
+    WinRun r{first, 0, 0, INT_MAX, 0, 0, INT_MAX, 0, INT_MAX};
+    for (int j = lane; j < nr; j += 32) {
+      const Visible v(tb.len[j], window, n_sink);
+      tb.run[j] = v.L > 0 ? 0 : -1;
+      if (v.L <= 0) continue;
+      r.base = min(r.base, v.w0);
+      r.ns = max(r.ns, v.ns);
+      r.end = max(r.end, v.L);
+      r.ns_min = min(r.ns_min, v.ns);
+      r.w0_max = max(r.w0_max, v.w0);
+      r.end_min = min(r.end_min, v.L);
+    }
+    r.base = __reduce_min_sync(0xffffffffu, r.base);
+    r.ns = __reduce_max_sync(0xffffffffu, r.ns);
+    r.end = __reduce_max_sync(0xffffffffu, r.end);
+    r.ns_min = __reduce_min_sync(0xffffffffu, r.ns_min);
+    r.w0_max = __reduce_max_sync(0xffffffffu, r.w0_max);
+    r.end_min = __reduce_min_sync(0xffffffffu, r.end_min);
+    if (lane == 0) {
+      tb.nruns = first < 0 ? 0 : 1;
+      tb.runs[0].tiles0 = 0;
+      if (first >= 0) {
+        tb.runs[1].tiles0 = finish(r, 0);
+        tb.runs[0] = r;
+      }
+    }
+    return;
+  }
+  if (lane) return;
+  int n = 0;
+  for (int j = 0; j < nr; ++j) {
+    const Visible v(tb.len[j], window, n_sink);
+    tb.run[j] = -1;
+    if (v.L <= 0) continue;
+    if (n == 0 || tb.runs[n - 1].seq != tb.seq[j])
+      tb.runs[n++] = WinRun{tb.seq[j], 0, 0, v.w0, v.ns, v.L, v.ns, v.w0, v.L};
+    WinRun& r = tb.runs[n - 1];
+    tb.run[j] = n - 1;
+    r.base = min(r.base, v.w0);
+    r.ns = max(r.ns, v.ns);
+    r.end = max(r.end, v.L);
+    r.ns_min = min(r.ns_min, v.ns);
+    r.w0_max = max(r.w0_max, v.w0);
+    r.end_min = min(r.end_min, v.L);
+  }
+  int tiles = 0;
+  for (int k = 0; k < n; ++k) tiles = finish(tb.runs[k], tiles);
+  tb.runs[n].tiles0 = tiles;
+  tb.nruns = n;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]: A is M = 128 rows of f16, row r in lane r, two k a column.
+__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// A pair's output row or partial record from its sums over this CTA's tiles: element d of acc.
+template <int D>
+struct WinOut {
+  const PartialParams& p;
+  int t, head, c;
+  float m, l, f;  // maximum in log2 units, sum, factor of the accumulator
+  bool nan;       // the sum is NaN: see keep_nan
+  float* dst;
+  __device__ __forceinline__ WinOut(const PartialParams& p_, int t_, int head_, int c_, float m_,
+                                    float l_)
+      : p(p_), t(t_), head(head_), c(c_), m(m_), l(l_), nan(l_ != l_) {
+    if (nan) {
+      m = kNanMax;
+      l = INFINITY;
+    }
+    f = p.merge ? 1.f : 1.f / l;
+    dst = p.merge ? p.part + (((size_t)t * p.n_split + c) * p.n_heads + head) * (D + 2)
+                  : p.out + ((size_t)t * p.n_heads + head) * D;
+  }
+  // l is 0 where the row saw nothing: acc may then hold 0 times a hidden value
+  __device__ __forceinline__ float value(int d, float acc) const {
+    const float y = nan ? __int_as_float(0x7fffffff) : l > 0.f ? acc * f : 0.f;
+    return p.merge ? y : gated(p, t, head, d, y);
+  }
+  __device__ __forceinline__ void stats() const {
+    if (!p.merge) return;
+    dst[D] = m == -INFINITY ? -INFINITY : m * kLn2;  // natural-log units
+    dst[D + 1] = l;
+  }
+};
+
+// The group's pairs over tiles [i0, i1), position by position, hidden ones skipped: a warp a pair.
+template <int D>
+__device__ void rows_plain(const PartialParams& p, const WinRowsTable& tb, int t0, int nr, int g,
+                           int c, int i0, int i1, int warp, int lane) {
+  constexpr int DPL = D / 32;
+  const int G = p.group;
+  const __half* kc = static_cast<const __half*>(p.kc);
+  const __half* vc = static_cast<const __half*>(p.vc);
+  for (int pair = warp; pair < nr * G; pair += WinRowsCfg<D>::NSW) {
+    const int row = pair / G, t = t0 + row, head = g * G + pair % G;
+    const Visible v(tb.len[row], p.window, p.n_sink);
+    float q[DPL], o[DPL], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int e = 0; e < DPL; ++e) {
+      q[e] = __ldg(p.q + ((size_t)t * p.n_heads + head) * D + lane * DPL + e) * p.scale_log2;
+      o[e] = 0.f;
+    }
+    int k = 0;
+    for (int i = i0; i < i1; ++i) {
+      const WinTile w = win_tile(tb, i, k);
+      if (k != tb.run[row]) continue;
+      const int e1 = min(min(w.start + kWinRowsTile, w.end), v.L);
+      for (int pos = w.start; pos < e1; ++pos) {
+        if (pos < v.w0 && pos >= v.ns) continue;
+        const size_t at = (((size_t)w.seq * p.cache_cap + pos) * p.n_kv_heads + g) * D + lane * DPL;
+        float x = 0.f;
+#pragma unroll
+        for (int e = 0; e < DPL; ++e) x = fmaf(q[e], __half2float(kc[at + e]), x);
+        x = warp_sum(x);
+        const float mn = fmaxf(m, x);
+        const float corr = m == -INFINITY ? 0.f : fast_exp2(m - mn), wgt = fast_exp2(x - mn);
+        m = mn;
+        l = l * corr + wgt;
+#pragma unroll
+        for (int e = 0; e < DPL; ++e) o[e] = fmaf(wgt, __half2float(vc[at + e]), o[e] * corr);
+      }
+    }
+    const WinOut<D> out(p, t, head, c, m, l);
+#pragma unroll
+    for (int e = 0; e < DPL; ++e) out.dst[lane * DPL + e] = out.value(lane * DPL + e, o[e]);
+    if (lane == 0) out.stats();
+  }
+}
+
+// tcgen05.wait::ld, and no use of the loaded registers moves above it.
+template <int N>
+__device__ __forceinline__ void tmem_ld_landed(uint32_t (&r)[N]) {
+  tmem_ld_wait();
+#pragma unroll
+  for (int e = 0; e < N; ++e) asm volatile("" : "+r"(r[e]));
+}
+
+template <int D>
+__global__ void __launch_bounds__(WinRowsCfg<D>::THREADS, 1)
+    window_rows_kernel(const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, const PartialParams p) {
+  using C = WinRowsCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ WinRowsTable tb;
+  const int c = blockIdx.x, g = blockIdx.y;
+  const int G = p.group, R = C::M / G;
+  const int t0 = blockIdx.z * R, nr = min(R, p.n_tok - t0);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  // ---- the rows, their runs and this CTA's tiles
+  if (threadIdx.x < nr) {
+    int s = 0;
+    tb.len[threadIdx.x] = visible_row(p, t0 + threadIdx.x, c == 0 && g == 0, s);
+    tb.seq[threadIdx.x] = s;
+  }
+  if (threadIdx.x == 0) tb.dirty = 0;
+  __syncthreads();
+  if (warp == 0) win_build(tb, nr, p.window, p.n_sink, lane);
+  __syncthreads();
+  const int n = tb.runs[tb.nruns].tiles0;
+  const int per = max((n + p.n_split - 1) / p.n_split, 1);
+  const int i0 = c * per, i1 = min(i0 + per, n);
+  if (c == 0 && g == 0 && p.merge && threadIdx.x < nr)
+    p.n_valid[t0 + threadIdx.x] = (n + per - 1) / per;
+  if (i0 >= i1) {
+    if (c == 0 && !p.merge)  // no row sees anything: zeros (a merge writes them otherwise)
+      for (int i = threadIdx.x; i < nr * G * D; i += C::THREADS)
+        p.out[((size_t)(t0 + i / (G * D)) * p.n_heads + g * G) * D + i % (G * D)] = 0.f;
+    return;
+  }
+  const int nt = i1 - i0;
+
+  const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
+  uint8_t* sK = smem_raw + pad;
+  uint8_t* sV = sK + C::NK * C::KT;
+  uint8_t* sQ = sK + C::Q_OFF;  // [hi, lo][box][128 rows][128 bytes]
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(sK + C::BAR_OFF);
+  uint64_t* k_empty = k_full + C::NK;
+  uint64_t* v_full = k_empty + C::NK;
+  uint64_t* v_empty = v_full + C::NV;
+  uint64_t* s_full = v_empty + C::NV;
+  uint64_t* p_full = s_full + C::NB;
+  uint64_t* pv_done = p_full + C::NB;
+  uint64_t* q_full = pv_done + C::NB;
+  uint64_t* drain = q_full + 1;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::NK; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < C::NV; ++i) {
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < C::NB; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 32 * C::NSW);
+      mbar_init(&pv_done[i], 1);
+    }
+    mbar_init(q_full, 32 * C::NSW);
+    mbar_init(drain, 1);
+    mbar_init_fence();
+  }
+  if (warp == C::ISSUER) tmem_alloc(tmem_holder, C::TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_holder;
+
+  if (warp == C::PRODUCER) {  // ---- TMA: K(j), then V(j - 1)
+    if (lane == 0) {
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+      bool ok = true;
+      int kk = 0, kv = 0, nk = 0, nv = 0;
+      for (int j = 0; j <= nt && ok; ++j) {
+        if (j < nt) {
+          const int st = j % C::NK;
+          ok = j < C::NK || mbar_wait(&k_empty[st], ((j / C::NK) - 1) & 1);
+          if (!ok) break;
+          const WinTile w = win_tile(tb, i0 + j, kk);
+          mbar_arrive_expect_tx(&k_full[st], C::KT);
+          for (int b = 0; b < C::NBOX; ++b)
+            tma_load_3d(sK + st * C::KT + b * C::BOX, &tmK, b * 64, g,
+                        w.seq * static_cast<int>(p.cache_cap) + w.start, &k_full[st]);
+          nk = j + 1;
+        }
+        if (j > 0) {
+          const int i = j - 1, st = i % C::NV;
+          ok = i < C::NV || mbar_wait(&v_empty[st], ((i / C::NV) - 1) & 1);
+          if (!ok) break;
+          const WinTile w = win_tile(tb, i0 + i, kv);
+          mbar_arrive_expect_tx(&v_full[st], C::KT);
+          for (int b = 0; b < C::NBOX; ++b)
+            tma_load_3d(sV + st * C::KT + b * C::BOX, &tmV, b * 64, g,
+                        w.seq * static_cast<int>(p.cache_cap) + w.start, &v_full[st]);
+          nv = i + 1;
+        }
+      }
+      // the last load of each slot lands before the CTA may leave
+      for (int st = 0; st < C::NK && st < nk; ++st)
+        ok = mbar_wait(&k_full[st], ((nk - 1 - st) / C::NK) & 1) && ok;
+      for (int st = 0; st < C::NV && st < nv; ++st)
+        ok = mbar_wait(&v_full[st], ((nv - 1 - st) / C::NV) & 1) && ok;
+      if (!ok) flag_error(p.err, GQA_ERR_TIMEOUT);
+    }
+  } else if (warp == C::ISSUER) {  // ---- MMAs: S(0), S(1), PV(0), S(2), PV(1), ...
+    if (lane == 0) {
+      constexpr uint32_t kIdS = umma_idesc_f16(C::M, C::TP, false);
+      constexpr uint32_t kIdO = umma_idesc_f16(C::M, D, true);
+      const uint32_t q_addr = smem_addr(sQ);
+      bool ok = mbar_wait(q_full, 0);
+      auto issue_s = [&](int j) {
+        const int st = j % C::NK, b = j % C::NB;
+        if (!mbar_wait(&k_full[st], (j / C::NK) & 1) ||
+            (j >= C::NB && !mbar_wait(&pv_done[b], ((j / C::NB) - 1) & 1)))
+          return false;
+        tc_fence_after();
+        const uint32_t sk = smem_addr(sK + st * C::KT);
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int kk = 0; kk < C::KS_S; ++kk)
+            umma_f16(tbase + b * C::TP,
+                     umma_desc_sw128(q_addr + part * C::Q_PART + (kk >> 2) * C::Q_BOX + (kk & 3) * 32,
+                                     16, 1024),
+                     umma_desc_sw128(sk + (kk >> 2) * C::BOX + (kk & 3) * 32, 16, 1024), kIdS,
+                     part + kk > 0 ? 1u : 0u);
+        umma_commit(&k_empty[st]);
+        umma_commit(&s_full[b]);
+        return true;
+      };
+      if (ok) ok = issue_s(0);
+      for (int j = 0; j < nt && ok; ++j) {
+        if (j + 1 < nt) ok = issue_s(j + 1);
+        const int st = j % C::NV, b = j % C::NB;
+        ok = ok && mbar_wait(&p_full[b], (j / C::NB) & 1) &&
+             mbar_wait(&v_full[st], (j / C::NV) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t sv = smem_addr(sV + st * C::KT);
+#pragma unroll
+        for (int kk = 0; kk < C::KS_O; ++kk)
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+            umma_f16_ta(tbase + C::O_COL, tbase + b * C::TP + part * (C::TP / 2) + kk * 8,
+                        umma_desc_sw128(sv + kk * 2048, C::BOX, 1024), kIdO,
+                        j + kk + part > 0 ? 1u : 0u);
+        umma_commit(&v_empty[st]);
+        umma_commit(&pv_done[b]);
+      }
+      umma_commit(drain);  // every MMA has completed before TMEM is freed
+      ok = mbar_wait(drain, 0) && ok;
+      if (!ok) flag_error(p.err, GQA_ERR_TIMEOUT);
+    }
+    __syncwarp();
+  } else {  // ---- softmax: thread i owns pair i = MMA row i
+    const int i = threadIdx.x;
+    const int row = i / G;
+    const bool rv = row < nr;
+    const int t = t0 + (rv ? row : 0), head = g * G + i % G;
+    const Visible vis(rv ? tb.len[row] : 0, p.window, p.n_sink);
+    const int run = rv ? tb.run[row] : -1;
+    const uint32_t t_row = tbase + (static_cast<uint32_t>(warp * 32) << 16);
+    // q: fp32 pieces of 16 bytes to f16 hi and lo, 128-byte swizzled
+    for (int f = i; f < C::M * (D / 4); f += 32 * C::NSW) {
+      const int qr = f / (D / 4), c4 = f % (D / 4), r = qr / G;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < nr)
+        x = __ldg(reinterpret_cast<const float4*>(
+                      p.q + ((size_t)(t0 + r) * p.n_heads + g * G + qr % G) * D) + c4);
+      uint2 hv, lv;
+      split_hi_lo(x.x * p.scale_log2, x.y * p.scale_log2, hv.x, lv.x);
+      split_hi_lo(x.z * p.scale_log2, x.w * p.scale_log2, hv.y, lv.y);
+      const int ch = c4 >> 1;
+      uint8_t* dst = sQ + (ch >> 3) * C::Q_BOX + qr * 128 + (((ch & 7) ^ (qr & 7)) << 4) +
+                     (c4 & 1) * 8;
+      *reinterpret_cast<uint2*>(dst) = hv;
+      *reinterpret_cast<uint2*>(dst + C::Q_PART) = lv;
+    }
+    fence_async_smem();
+    mbar_arrive(q_full);
+
+    // After a wait has run out none is tried again, but every warp walks all tiles, so that the
+    // barriers of the epilogue are met; the call flags GQA_ERR_TIMEOUT.
+    bool ok = true;
+    auto wait = [&ok](uint64_t* bar, uint32_t parity) {
+      if (ok) ok = __all_sync(0xffffffffu, mbar_test(bar, parity) || mbar_wait(bar, parity));
+    };
+    float m_run = -INFINITY, l_run = 0.f;
+    int k = 0;
+    for (int j = 0; j < nt; ++j) {
+      const int b = j % C::NB;
+      const WinTile w = win_tile(tb, i0 + j, k);
+      wait(&s_full[b], (j / C::NB) & 1);
+      tc_fence_after();
+      uint32_t s[C::TP];
+#pragma unroll
+      for (int q = 0; q < C::TP / 32; ++q)
+        tmem_ld32(t_row + b * C::TP + 32 * q, reinterpret_cast<uint32_t(&)[32]>(s[32 * q]));
+      tmem_ld_landed(s);
+      // columns the row sees: [lo, hi) and [0, ns)
+      const int hi = run == k ? min(vis.L, w.end) - w.start : 0;
+      const int lo = vis.w0 - w.start, ns = vis.ns - w.start;
+      const bool whole = hi >= C::TP && (lo <= 0 || ns >= C::TP);
+      if (!__all_sync(0xffffffffu, whole)) {
+#pragma unroll
+        for (int e = 0; e < C::TP; ++e)
+          if (e >= hi || (e < lo && e >= ns)) s[e] = 0xff800000u;  // -inf
+      }
+      float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int e = 0; e < C::TP; ++e) mq[e & 3] = fmaxf(mq[e & 3], __uint_as_float(s[e]));
+      const float mt = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+      const bool grow = mt > m_run + C::RESCALE_LOG2;
+      const bool resc = grow && m_run != -INFINITY;  // O holds weight
+      if (__any_sync(0xffffffffu, resc)) {
+        wait(&pv_done[(j - 1) % C::NB], ((j - 1) / C::NB) & 1);
+        tc_fence_after();
+        const float corr = resc ? ex2_approx(m_run - mt) : 1.f;
+#pragma unroll 1
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t o[32];
+          tmem_ld32(t_row + C::O_COL + 32 * q, o);
+          tmem_ld_landed(o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+          tmem_st32(t_row + C::O_COL + 32 * q, o);
+        }
+        l_run *= corr;
+      }
+      if (grow) m_run = mt;
+      const float mu = m_run == -INFINITY ? 0.f : m_run;
+      float lq[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {  // 64 positions: 32 columns of P hi, 32 of P lo
+        uint32_t ph[32], pl[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float w0 = ex2_approx(__uint_as_float(s[64 * q + 2 * e]) - mu);
+          const float w1 = ex2_approx(__uint_as_float(s[64 * q + 2 * e + 1]) - mu);
+          lq[e & 3] += w0 + w1;
+          split_hi_lo(w0, w1, ph[e], pl[e]);
+        }
+        tmem_st32(t_row + b * C::TP + 32 * q, ph);
+        tmem_st32(t_row + b * C::TP + C::TP / 2 + 32 * q, pl);
+      }
+      l_run += (lq[0] + lq[1]) + (lq[2] + lq[3]);
+      tmem_st_wait();
+      // V rows behind the run's positions are zeroed; a tile that some row of the group does not
+      // see whole is searched for values that are not finite
+      const int nvis = min(C::TP, w.end - w.start);
+      const WinRun& r = tb.runs[k];
+      const bool all_see = tb.nruns == 1 && ((w.start >= r.w0_max && w.start + nvis <= r.end_min) ||
+                                             w.start + nvis <= r.ns_min);
+      if (nvis < C::TP || !all_see) {
+        const int st = j % C::NV;
+        wait(&v_full[st], (j / C::NV) & 1);
+        uint8_t* v = sV + st * C::KT;
+        bool bad = false;
+        for (int e = i; e < C::NBOX * C::TP * 8; e += 32 * C::NSW) {  // 16-byte pieces
+          uint4* x = reinterpret_cast<uint4*>(v + e * 16);
+          if ((e / 8) % C::TP >= nvis) {
+            *x = make_uint4(0u, 0u, 0u, 0u);
+          } else if (!all_see) {
+            const uint4 y = *x;  // a half is not finite if its magnitude is 0x7c00 or more
+            bad |= ((((y.x & 0x7fff7fffu) + 0x04000400u) | ((y.y & 0x7fff7fffu) + 0x04000400u) |
+                     ((y.z & 0x7fff7fffu) + 0x04000400u) | ((y.w & 0x7fff7fffu) + 0x04000400u)) &
+                    0x80008000u) != 0;
+          }
+        }
+        if (bad) tb.dirty = 1;
+        fence_async_smem();
+      }
+      tc_fence_before();
+      mbar_arrive(&p_full[b]);
+    }
+
+    // ---- O of the last tile, to the output or the chunk's partial
+    wait(&pv_done[(nt - 1) % C::NB], ((nt - 1) / C::NB) & 1);
+    tc_fence_after();
+    const WinOut<D> out(p, t, head, c, m_run, l_run);
+#pragma unroll 1
+    for (int q = 0; q < D / 32; ++q) {
+      uint32_t o[32];
+      tmem_ld32(t_row + C::O_COL + 32 * q, o);
+      tmem_ld_landed(o);
+      if (rv) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 2)
+          *reinterpret_cast<float2*>(out.dst + 32 * q + e) =
+              make_float2(out.value(32 * q + e, __uint_as_float(o[e])),
+                          out.value(32 * q + e + 1, __uint_as_float(o[e + 1])));
+      }
+    }
+    if (rv) out.stats();
+    if (!ok && lane == 0) flag_error(p.err, GQA_ERR_TIMEOUT);
+    named_bar_sync(1, 32 * C::NSW);
+    if (tb.dirty) rows_plain<D>(p, tb, t0, nr, g, c, i0, i1, warp, lane);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::ISSUER) {
+    tc_fence_after();
+    tmem_free(tbase, C::TMEM_COLS);
+  }
+}
+
+template <int D>
+static cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const PartialParams& p,
+                            dim3 grid, cudaStream_t s) {
+  using C = WinRowsCfg<D>;
+  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(&window_rows_kernel<D>), C::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  cfg.attrs = at;
+  cfg.numAttrs = cluster_attrs(at, 0, 1);
+  return cudaLaunchKernelEx(&cfg, &window_rows_kernel<D>, tk, tv, p);
+}
+
+cudaError_t launch_window_rows(int head_dim, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const PartialParams& p, dim3 grid, cudaStream_t s) {
+  return head_dim == 64 ? launch_d<64>(tk, tv, p, grid, s) : launch_d<128>(tk, tv, p, grid, s);
+}
+
+}  // namespace gqa

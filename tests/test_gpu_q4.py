@@ -201,6 +201,22 @@ def test_decode_scales(k_scale, v_scale, scale, qmul):
     assert_close(got / v_scale, ref / v_scale, TOL, "scales")
 
 
+@pytest.mark.parametrize("chunk", [None, 64])
+def test_decode_nan_query(chunk):
+    """A row with a NaN in q comes out as NaN, the others as they are; an empty one as zeros."""
+    rng = np.random.default_rng(14)
+    lens = [300, 300, 0]
+    cache = q4_cache(rng, lens, 2, 304, 128)
+    q = rows(rng, 3, 8, 128)
+    q[0, 1, 77] = q[2, 1, 3] = np.nan
+    with forced_chunk(chunk):
+        got = run_q4(q, cache, lens).cpu().numpy()
+    assert np.isnan(got[0, 1]).all() and (got[2] == 0).all()
+    ref = oracle.decode_q4(np.nan_to_num(q), *cache, lens, 128 ** -0.5)
+    got[0, 1] = ref[0, 1]
+    assert_close(got, ref, TOL, "NaN query")
+
+
 def test_decode_bad_lengths_and_sequences():
     gd = _gd()
     rng = np.random.default_rng(5)

@@ -129,6 +129,60 @@ def test_prefill_chunk(D):
         assert_close(got, ref, TOL, f"chunk at {first}")
 
 
+@pytest.mark.parametrize("H,Hk,D,T", [(8, 2, 128, 150), (2, 2, 64, 200), (32, 2, 64, 40),
+                                      (12, 1, 128, 33), (8, 2, 256, 20), (4, 2, 128, 5)])
+def test_values_that_some_rows_see(H, Hk, D, T):
+    """NaN and infinities in K and V at positions that some rows of a chunk see and others do not:
+    the others' outputs are what they are without them."""
+    rng = np.random.default_rng(T + D)
+    window, n_sink, first = 60, 3, 240
+    lens = [first + r for r in range(T)]
+    k, v = f16_cache(rng, 1, first + T, Hk, D)
+    q = rows(rng, T, H, D)
+    odd = [(first + 2, 0, 5, np.inf), (first - 40, Hk - 1, D - 1, np.nan), (first + T // 2, 0, 9, -np.inf)]
+    bad_k = first + T - 3                               # seen by the last rows only
+    clean_k, clean_v = k.copy(), v.copy()
+    for pos, g, d, x in odd:
+        v[0, pos, g, d], clean_v[0, pos, g, d] = x, 0
+    k[0, bad_k, :, 7] = np.nan
+    got = run(q, k, v, lens, window, n_sink, [0] * T).cpu().numpy()
+    ref = oracle.decode_f16_window(q, clean_k, clean_v, lens, D ** -0.5, window, n_sink,
+                                   seq_of=[0] * T)
+    G = H // Hk
+    fine = np.ones(got.shape, bool)
+    for t, n in enumerate(lens):
+        see = set(oracle.visible_positions(n, window, n_sink).tolist())
+        if bad_k in see:
+            fine[t] = False
+        for pos, g, d, _ in odd:
+            if pos in see:
+                fine[t, g * G:(g + 1) * G, d] = False
+    assert not np.isfinite(got[~fine]).any() and np.isfinite(got[fine]).all()
+    assert fine.any() and not fine.all()
+    assert_close(np.where(fine, got, 0), np.where(fine, ref, 0), TOL, "rows that do not see them")
+
+
+@pytest.mark.parametrize("H,Hk,D", [(2, 2, 64), (8, 2, 128), (32, 2, 128), (12, 2, 64)])
+def test_many_rows_of_several_sequences(H, Hk, D):
+    """300 rows in runs of 1 to 60 of five sequences, lengths from 0 on: several runs in a group, a
+    run over several groups; a grid split over positions and one that is not."""
+    rng = np.random.default_rng(D + H)
+    seq, lens = [], []
+    while len(seq) < 300:
+        s, m, n0 = int(rng.integers(5)), int(rng.integers(1, 61)), int(rng.integers(0, 900))
+        seq += [s] * m
+        lens += [min(960, n0 + i) for i in range(m)]
+    seq, lens = seq[:300], lens[:300]
+    k, v = f16_cache(rng, 5, 960, Hk, D)
+    q = rows(rng, 300, H, D)
+    for window, n_sink in ((150, 4), (5000, 0), (33, 200)):
+        for T in (300, 40):
+            got = run(q[:T], k, v, lens[:T], window, n_sink, seq[:T]).cpu().numpy()
+            ref = oracle.decode_f16_window(q[:T], k, v, lens[:T], D ** -0.5, window, n_sink,
+                                           seq_of=seq[:T])
+            assert_close(got, ref, TOL, f"window {window} rows {T}")
+
+
 def test_large_scores_and_infinite_values_in_sight():
     """Scores of many thousands keep one position; an infinite V in sight leaves its dim without a
     finite value, one hidden does not.  (Which one is open: a weight w goes into the product as
