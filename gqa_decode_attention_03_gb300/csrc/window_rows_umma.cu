@@ -2,13 +2,13 @@
 // on the fifth-generation tensor cores.
 //
 // One CTA serves the 128 / G consecutive query rows of a group for one KV head: their (row, head)
-// pairs are the M = 128 rows of its MMAs, one softmax thread each, so every K/V tile is read once
+// pairs are the M = 128 rows of its MMAs, two softmax threads each, so every K/V tile is read once
 // for all of them.  Per tile of 128 positions
 //   S  = Q . K^T     fp32 in TMEM; Q (scale * log2 e folded in) as f16 hi + f16 lo, two MMAs a
 //                    k-step into the same S
-//   P  = 2^(S - m)   by the row's thread: masked by its own row's window, the running maximum
-//                    moves only when a tile exceeds it by 2^8; written back over S in TMEM as f16
-//                    hi and lo parts (64 columns each)
+//   P  = 2^(S - m)   by the row's two threads, 64 positions each: masked by the row's own window,
+//                    the running maximum moves only when a tile exceeds it by 2^8; written back
+//                    over S in TMEM as f16 hi and lo parts (64 columns each)
 //   O += P . V       fp32 in TMEM, A = P from TMEM, two MMAs a k-step
 // hi + lo keep ~22 bits of q and of the weights; K and V are f16 as they are.
 //
@@ -38,8 +38,8 @@ struct WinRowsCfg {
   static constexpr int Q_BOX = M * 128, Q_PART = NBOX * Q_BOX;
   static constexpr int NB = 3;                     // S/P buffers in TMEM
   static constexpr int O_COL = NB * TP, TMEM_COLS = 512;
-  static constexpr int KS_S = D / 16, KS_O = TP / 16;
-  static constexpr int NSW = 4, PRODUCER = 4, ISSUER = 5, THREADS = 192;
+  static constexpr int KS_S = D / 16;
+  static constexpr int NSW = 8, PRODUCER = 8, ISSUER = 9, THREADS = 320;
   static constexpr int Q_OFF = (NK + NV) * KT;
   static constexpr int NBAR = 2 * NK + 2 * NV + 3 * NB + 2;
   static constexpr int BAR_OFF = Q_OFF + 2 * Q_PART;
@@ -63,6 +63,7 @@ struct WinRowsTable {
   int run[128];    // row -> its run, -1 for a row that sees nothing
   WinRun runs[129];  // runs[nruns].tiles0: the number of tiles
   int nruns, dirty;
+  float mx[2][2][128];  // [tile parity][half][row]: maxima of the halves; at the end their sums
 };
 
 struct WinTile {
@@ -236,6 +237,16 @@ __device__ void rows_plain(const PartialParams& p, const WinRowsTable& tb, int t
   }
 }
 
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {  // one instruction for two sums
+  float2 r;
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
 // tcgen05.wait::ld, and no use of the loaded registers moves above it.
 template <int N>
 __device__ __forceinline__ void tmem_ld_landed(uint32_t (&r)[N]) {
@@ -358,12 +369,17 @@ __global__ void __launch_bounds__(WinRowsCfg<D>::THREADS, 1)
     }
   } else if (warp == C::ISSUER) {  // ---- MMAs: S(0), S(1), PV(0), S(2), PV(1), ...
     if (lane == 0) {
-      constexpr uint32_t kIdS = umma_idesc_f16(C::M, C::TP, false);
       constexpr uint32_t kIdO = umma_idesc_f16(C::M, D, true);
       const uint32_t q_addr = smem_addr(sQ);
       bool ok = mbar_wait(q_full, 0);
+      int ks = 0, ko = 0;  // runs of the next S and PV
+      auto steps = [&](int j, int& k) {  // 16-position steps of tile j that hold positions
+        const WinTile w = win_tile(tb, i0 + j, k);
+        return (min(C::TP, w.end - w.start) + 15) / 16;
+      };
       auto issue_s = [&](int j) {
         const int st = j % C::NK, b = j % C::NB;
+        const uint32_t id = umma_idesc_f16(C::M, 16 * steps(j, ks), false);
         if (!mbar_wait(&k_full[st], (j / C::NK) & 1) ||
             (j >= C::NB && !mbar_wait(&pv_done[b], ((j / C::NB) - 1) & 1)))
           return false;
@@ -376,7 +392,7 @@ __global__ void __launch_bounds__(WinRowsCfg<D>::THREADS, 1)
             umma_f16(tbase + b * C::TP,
                      umma_desc_sw128(q_addr + part * C::Q_PART + (kk >> 2) * C::Q_BOX + (kk & 3) * 32,
                                      16, 1024),
-                     umma_desc_sw128(sk + (kk >> 2) * C::BOX + (kk & 3) * 32, 16, 1024), kIdS,
+                     umma_desc_sw128(sk + (kk >> 2) * C::BOX + (kk & 3) * 32, 16, 1024), id,
                      part + kk > 0 ? 1u : 0u);
         umma_commit(&k_empty[st]);
         umma_commit(&s_full[b]);
@@ -391,8 +407,9 @@ __global__ void __launch_bounds__(WinRowsCfg<D>::THREADS, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t sv = smem_addr(sV + st * C::KT);
-#pragma unroll
-        for (int kk = 0; kk < C::KS_O; ++kk)
+        const int nk = steps(j, ko);
+#pragma unroll 4
+        for (int kk = 0; kk < nk; ++kk)
 #pragma unroll
           for (int part = 0; part < 2; ++part)
             umma_f16_ta(tbase + C::O_COL, tbase + b * C::TP + part * (C::TP / 2) + kk * 8,
@@ -406,16 +423,17 @@ __global__ void __launch_bounds__(WinRowsCfg<D>::THREADS, 1)
       if (!ok) flag_error(p.err, GQA_ERR_TIMEOUT);
     }
     __syncwarp();
-  } else {  // ---- softmax: thread i owns pair i = MMA row i
-    const int i = threadIdx.x;
+  } else {  // ---- softmax: threads (h, i), h = 0, 1, own pair i = MMA row i
+    const int h = warp >> 2, i = threadIdx.x & 127;
     const int row = i / G;
     const bool rv = row < nr;
     const int t = t0 + (rv ? row : 0), head = g * G + i % G;
     const Visible vis(rv ? tb.len[row] : 0, p.window, p.n_sink);
     const int run = rv ? tb.run[row] : -1;
-    const uint32_t t_row = tbase + (static_cast<uint32_t>(warp * 32) << 16);
+    const uint32_t t_row = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     // q: fp32 pieces of 16 bytes to f16 hi and lo, 128-byte swizzled
-    for (int f = i; f < C::M * (D / 4); f += 32 * C::NSW) {
+#pragma unroll 4
+    for (int f = threadIdx.x; f < C::M * (D / 4); f += 32 * C::NSW) {
       const int qr = f / (D / 4), c4 = f % (D / 4), r = qr / G;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < nr)
@@ -446,58 +464,70 @@ __global__ void __launch_bounds__(WinRowsCfg<D>::THREADS, 1)
       const WinTile w = win_tile(tb, i0 + j, k);
       wait(&s_full[b], (j / C::NB) & 1);
       tc_fence_after();
-      uint32_t s[C::TP];
-#pragma unroll
-      for (int q = 0; q < C::TP / 32; ++q)
-        tmem_ld32(t_row + b * C::TP + 32 * q, reinterpret_cast<uint32_t(&)[32]>(s[32 * q]));
+      uint32_t s[64];  // columns 64 h ..
+      tmem_ld32(t_row + b * C::TP + 64 * h, reinterpret_cast<uint32_t(&)[32]>(s[0]));
+      tmem_ld32(t_row + b * C::TP + 64 * h + 32, reinterpret_cast<uint32_t(&)[32]>(s[32]));
       tmem_ld_landed(s);
       // columns the row sees: [lo, hi) and [0, ns)
-      const int hi = run == k ? min(vis.L, w.end) - w.start : 0;
-      const int lo = vis.w0 - w.start, ns = vis.ns - w.start;
-      const bool whole = hi >= C::TP && (lo <= 0 || ns >= C::TP);
+      const int c0 = w.start + 64 * h;
+      const int hi = run == k ? min(vis.L, w.end) - c0 : 0;
+      const int lo = vis.w0 - c0, ns = vis.ns - c0;
+      const bool whole = hi >= 64 && (lo <= 0 || ns >= 64);
       if (!__all_sync(0xffffffffu, whole)) {
 #pragma unroll
-        for (int e = 0; e < C::TP; ++e)
+        for (int e = 0; e < 64; ++e)
           if (e >= hi || (e < lo && e >= ns)) s[e] = 0xff800000u;  // -inf
       }
       float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int e = 0; e < C::TP; ++e) mq[e & 3] = fmaxf(mq[e & 3], __uint_as_float(s[e]));
-      const float mt = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+      for (int e = 0; e < 64; ++e) mq[e & 3] = fmaxf(mq[e & 3], __uint_as_float(s[e]));
+      float mt = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+      // the row's other half: its maximum, and the word that it has read its columns of S, over
+      // which both halves write P
+      tb.mx[j & 1][h][i] = mt;
+      tc_fence_before();
+      named_bar_sync(2 + (warp & 3), 64);
+      tc_fence_after();
+      mt = fmaxf(mt, tb.mx[j & 1][h ^ 1][i]);
       const bool grow = mt > m_run + C::RESCALE_LOG2;
       const bool resc = grow && m_run != -INFINITY;  // O holds weight
-      if (__any_sync(0xffffffffu, resc)) {
+      if (__any_sync(0xffffffffu, resc)) {           // (the same in both halves' warps)
         wait(&pv_done[(j - 1) % C::NB], ((j - 1) / C::NB) & 1);
         tc_fence_after();
         const float corr = resc ? ex2_approx(m_run - mt) : 1.f;
 #pragma unroll 1
-        for (int q = 0; q < D / 32; ++q) {
+        for (int q = 0; q < D / 64; ++q) {  // this half's D / 2 columns
+          const uint32_t col = t_row + C::O_COL + h * (D / 2) + 32 * q;
           uint32_t o[32];
-          tmem_ld32(t_row + C::O_COL + 32 * q, o);
+          tmem_ld32(col, o);
           tmem_ld_landed(o);
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-          tmem_st32(t_row + C::O_COL + 32 * q, o);
+          tmem_st32(col, o);
         }
         l_run *= corr;
       }
       if (grow) m_run = mt;
       const float mu = m_run == -INFINITY ? 0.f : m_run;
-      float lq[4] = {0.f, 0.f, 0.f, 0.f};
+      float2 lq[2] = {{0.f, 0.f}, {0.f, 0.f}};
+      uint32_t ph[32], pl[32];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {  // 64 positions: 32 columns of P hi, 32 of P lo
-        uint32_t ph[32], pl[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float w0 = ex2_approx(__uint_as_float(s[64 * q + 2 * e]) - mu);
-          const float w1 = ex2_approx(__uint_as_float(s[64 * q + 2 * e + 1]) - mu);
-          lq[e & 3] += w0 + w1;
-          split_hi_lo(w0, w1, ph[e], pl[e]);
-        }
-        tmem_st32(t_row + b * C::TP + 32 * q, ph);
-        tmem_st32(t_row + b * C::TP + C::TP / 2 + 32 * q, pl);
+      for (int e = 0; e < 32; ++e) {
+        float2 x = add2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])),
+                        make_float2(-mu, -mu));
+        x.x = ex2_approx(x.x);
+        x.y = ex2_approx(x.y);
+        lq[e & 1] = add2(lq[e & 1], x);
+        const __half2 hv = __floats2half2_rn(x.x, x.y);
+        const float2 hf = __half22float2(hv);
+        ph[e] = h2_bits(hv);
+        const float2 lv = add2(x, make_float2(-hf.x, -hf.y));
+        pl[e] = h2_bits(__floats2half2_rn(lv.x, lv.y));
       }
-      l_run += (lq[0] + lq[1]) + (lq[2] + lq[3]);
+      tmem_st32(t_row + b * C::TP + 32 * h, ph);
+      tmem_st32(t_row + b * C::TP + C::TP / 2 + 32 * h, pl);
+      lq[0] = add2(lq[0], lq[1]);
+      l_run += lq[0].x + lq[0].y;
       tmem_st_wait();
       // V rows behind the run's positions are zeroed; a tile that some row of the group does not
       // see whole is searched for values that are not finite
@@ -510,7 +540,7 @@ __global__ void __launch_bounds__(WinRowsCfg<D>::THREADS, 1)
         wait(&v_full[st], (j / C::NV) & 1);
         uint8_t* v = sV + st * C::KT;
         bool bad = false;
-        for (int e = i; e < C::NBOX * C::TP * 8; e += 32 * C::NSW) {  // 16-byte pieces
+        for (int e = threadIdx.x; e < C::NBOX * C::TP * 8; e += 32 * C::NSW) {  // 16-byte pieces
           uint4* x = reinterpret_cast<uint4*>(v + e * 16);
           if ((e / 8) % C::TP >= nvis) {
             *x = make_uint4(0u, 0u, 0u, 0u);
@@ -528,24 +558,28 @@ __global__ void __launch_bounds__(WinRowsCfg<D>::THREADS, 1)
       mbar_arrive(&p_full[b]);
     }
 
-    // ---- O of the last tile, to the output or the chunk's partial
+    // ---- O of the last tile, to the output or the chunk's partial: a half of the dims each
+    tb.mx[nt & 1][h][i] = l_run;
+    named_bar_sync(2 + (warp & 3), 64);
+    l_run += tb.mx[nt & 1][h ^ 1][i];
     wait(&pv_done[(nt - 1) % C::NB], ((nt - 1) / C::NB) & 1);
     tc_fence_after();
     const WinOut<D> out(p, t, head, c, m_run, l_run);
 #pragma unroll 1
-    for (int q = 0; q < D / 32; ++q) {
+    for (int q = 0; q < D / 64; ++q) {
+      const int d0 = h * (D / 2) + 32 * q;
       uint32_t o[32];
-      tmem_ld32(t_row + C::O_COL + 32 * q, o);
+      tmem_ld32(t_row + C::O_COL + d0, o);
       tmem_ld_landed(o);
       if (rv) {
 #pragma unroll
         for (int e = 0; e < 32; e += 2)
-          *reinterpret_cast<float2*>(out.dst + 32 * q + e) =
-              make_float2(out.value(32 * q + e, __uint_as_float(o[e])),
-                          out.value(32 * q + e + 1, __uint_as_float(o[e + 1])));
+          *reinterpret_cast<float2*>(out.dst + d0 + e) =
+              make_float2(out.value(d0 + e, __uint_as_float(o[e])),
+                          out.value(d0 + e + 1, __uint_as_float(o[e + 1])));
       }
     }
-    if (rv) out.stats();
+    if (rv && h == 0) out.stats();
     if (!ok && lane == 0) flag_error(p.err, GQA_ERR_TIMEOUT);
     named_bar_sync(1, 32 * C::NSW);
     if (tb.dirty) rows_plain<D>(p, tb, t0, nr, g, c, i0, i1, warp, lane);
