@@ -39,7 +39,7 @@ struct WinRowsCfg {
   static constexpr int NB = 3;                     // S/P buffers in TMEM
   static constexpr int O_COL = NB * TP, TMEM_COLS = 512;
   static constexpr int KS_S = D / 16;
-  static constexpr int NSW = 8, PRODUCER = 8, ISSUER = 9, THREADS = 320;
+  static constexpr int NSW = 8, PRODUCER = 8, ISSUER = 9, PV_ISSUER = 10, THREADS = 352;
   static constexpr int Q_OFF = (NK + NV) * KT;
   static constexpr int NBAR = 2 * NK + 2 * NV + 3 * NB + 2;
   static constexpr int BAR_OFF = Q_OFF + 2 * Q_PART;
@@ -64,6 +64,7 @@ struct WinRowsTable {
   WinRun runs[129];  // runs[nruns].tiles0: the number of tiles
   int nruns, dirty;
   float mx[2][2][128];  // [tile parity][half][row]: maxima of the halves; at the end their sums
+  float m[128], l[128];  // the pairs' final state
 };
 
 struct WinTile {
@@ -82,7 +83,8 @@ __device__ __forceinline__ WinTile win_tile(const WinRowsTable& tb, int i, int& 
   return w;
 }
 
-// Thread-serial or warp-wide (one sequence) construction of the runs; warp 0.
+// The runs of the group's rows, by one warp: together where they all belong to one sequence, else by
+// its first lane.
 __device__ void win_build(WinRowsTable& tb, int nr, int window, int n_sink, int lane) {
   auto finish = [](WinRun& r, int tiles0) {
     r.tiles0 = tiles0;
@@ -269,29 +271,6 @@ __global__ void __launch_bounds__(WinRowsCfg<D>::THREADS, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
 
-  // ---- the rows, their runs and this CTA's tiles
-  if (threadIdx.x < nr) {
-    int s = 0;
-    tb.len[threadIdx.x] = visible_row(p, t0 + threadIdx.x, c == 0 && g == 0, s);
-    tb.seq[threadIdx.x] = s;
-  }
-  if (threadIdx.x == 0) tb.dirty = 0;
-  __syncthreads();
-  if (warp == 0) win_build(tb, nr, p.window, p.n_sink, lane);
-  __syncthreads();
-  const int n = tb.runs[tb.nruns].tiles0;
-  const int per = max((n + p.n_split - 1) / p.n_split, 1);
-  const int i0 = c * per, i1 = min(i0 + per, n);
-  if (c == 0 && g == 0 && p.merge && threadIdx.x < nr)
-    p.n_valid[t0 + threadIdx.x] = (n + per - 1) / per;
-  if (i0 >= i1) {
-    if (c == 0 && !p.merge)  // no row sees anything: zeros (a merge writes them otherwise)
-      for (int i = threadIdx.x; i < nr * G * D; i += C::THREADS)
-        p.out[((size_t)(t0 + i / (G * D)) * p.n_heads + g * G) * D + i % (G * D)] = 0.f;
-    return;
-  }
-  const int nt = i1 - i0;
-
   const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
   uint8_t* sK = smem_raw + pad;
   uint8_t* sV = sK + C::NK * C::KT;
@@ -303,37 +282,86 @@ __global__ void __launch_bounds__(WinRowsCfg<D>::THREADS, 1)
   uint64_t* s_full = v_empty + C::NV;
   uint64_t* p_full = s_full + C::NB;
   uint64_t* pv_done = p_full + C::NB;
-  uint64_t* q_full = pv_done + C::NB;
-  uint64_t* drain = q_full + 1;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < C::NK; ++i) {
-      mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 1);
+  uint64_t* drain = pv_done + C::NB;  // [2]: one per issuing thread
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 2);
+
+  // ---- at once: the softmax warps bring q in, the producer finds the rows' runs and sets the
+  //      barriers up, the issuer takes tensor memory
+  if (warp < C::NSW) {
+    // q: fp32 pieces of 16 bytes (all loads first) to f16 hi and lo, 128-byte swizzled
+    constexpr int NQ = C::M * (D / 4) / (32 * C::NSW);
+    float4 x[NQ];
+#pragma unroll
+    for (int u = 0; u < NQ; ++u) {
+      const unsigned f = threadIdx.x + u * 32 * C::NSW, qr = f / (D / 4), r = qr / unsigned(G);
+      x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (static_cast<int>(r) < nr)
+        x[u] = __ldg(reinterpret_cast<const float4*>(
+                         p.q + ((size_t)(t0 + r) * p.n_heads + g * G + (qr - r * G)) * D) +
+                     f % (D / 4));
     }
-    for (int i = 0; i < C::NV; ++i) {
-      mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 1);
+#pragma unroll
+    for (int u = 0; u < NQ; ++u) {
+      const unsigned f = threadIdx.x + u * 32 * C::NSW, qr = f / (D / 4), c4 = f % (D / 4);
+      const unsigned ch = c4 >> 1;
+      uint2 hv, lv;
+      split_hi_lo(x[u].x * p.scale_log2, x[u].y * p.scale_log2, hv.x, lv.x);
+      split_hi_lo(x[u].z * p.scale_log2, x[u].w * p.scale_log2, hv.y, lv.y);
+      uint8_t* dst = sQ + (ch >> 3) * C::Q_BOX + qr * 128 + (((ch & 7) ^ (qr & 7)) << 4) +
+                     (c4 & 1) * 8;
+      *reinterpret_cast<uint2*>(dst) = hv;
+      *reinterpret_cast<uint2*>(dst + C::Q_PART) = lv;
     }
-    for (int i = 0; i < C::NB; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 32 * C::NSW);
-      mbar_init(&pv_done[i], 1);
+    fence_async_smem();
+  } else if (warp == C::PRODUCER) {
+    for (int j = lane; j < nr; j += 32) {
+      int s = 0;
+      tb.len[j] = visible_row(p, t0 + j, c == 0 && g == 0, s);
+      tb.seq[j] = s;
     }
-    mbar_init(q_full, 32 * C::NSW);
-    mbar_init(drain, 1);
-    mbar_init_fence();
+    if (lane == 0) {
+      tb.dirty = 0;
+      for (int i = 0; i < C::NK; ++i) {
+        mbar_init(&k_full[i], 1);
+        mbar_init(&k_empty[i], 1);
+      }
+      for (int i = 0; i < C::NV; ++i) {
+        mbar_init(&v_full[i], 1);
+        mbar_init(&v_empty[i], 1);
+      }
+      for (int i = 0; i < C::NB; ++i) {
+        mbar_init(&s_full[i], 1);
+        mbar_init(&p_full[i], 32 * C::NSW);
+        mbar_init(&pv_done[i], 1);
+      }
+      mbar_init(&drain[0], 1);
+      mbar_init(&drain[1], 1);
+      mbar_init_fence();
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
+    __syncwarp();
+    win_build(tb, nr, p.window, p.n_sink, lane);
+  } else if (warp == C::ISSUER) {
+    tmem_alloc(tmem_holder, C::TMEM_COLS);
   }
-  if (warp == C::ISSUER) tmem_alloc(tmem_holder, C::TMEM_COLS);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_holder;
+  const int n = tb.runs[tb.nruns].tiles0;
+  const int per = max((n + p.n_split - 1) / p.n_split, 1);
+  const int i0 = c * per, i1 = min(i0 + per, n);
+  const int nt = i1 - i0;
+  if (c == 0 && g == 0 && p.merge && threadIdx.x < nr)
+    p.n_valid[t0 + threadIdx.x] = (n + per - 1) / per;
 
-  if (warp == C::PRODUCER) {  // ---- TMA: K(j), then V(j - 1)
+  if (nt <= 0) {
+    if (c == 0 && !p.merge)  // no row sees anything: zeros (a merge writes them otherwise)
+      for (int i = threadIdx.x; i < nr * G * D; i += C::THREADS)
+        p.out[((size_t)(t0 + i / (G * D)) * p.n_heads + g * G) * D + i % (G * D)] = 0.f;
+  } else if (warp == C::PRODUCER) {  // ---- TMA: K(j), then V(j - 1)
     if (lane == 0) {
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
       bool ok = true;
       int kk = 0, kv = 0, nk = 0, nv = 0;
       for (int j = 0; j <= nt && ok; ++j) {
@@ -367,59 +395,62 @@ __global__ void __launch_bounds__(WinRowsCfg<D>::THREADS, 1)
         ok = mbar_wait(&v_full[st], ((nv - 1 - st) / C::NV) & 1) && ok;
       if (!ok) flag_error(p.err, GQA_ERR_TIMEOUT);
     }
-  } else if (warp == C::ISSUER) {  // ---- MMAs: S(0), S(1), PV(0), S(2), PV(1), ...
+  } else if (warp == C::ISSUER || warp == C::PV_ISSUER) {
+    // ---- MMAs, lane 0 of two warps: one issues S, the other P . V (a thread that issues both
+    //      leaves the tensor cores idle while it waits between them)
+    const bool is_s = warp == C::ISSUER;
     if (lane == 0) {
-      constexpr uint32_t kIdO = umma_idesc_f16(C::M, D, true);
-      const uint32_t q_addr = smem_addr(sQ);
-      bool ok = mbar_wait(q_full, 0);
-      int ks = 0, ko = 0;  // runs of the next S and PV
-      auto steps = [&](int j, int& k) {  // 16-position steps of tile j that hold positions
+      bool ok = true;
+      int k = 0;
+      auto steps = [&](int j) {  // 16-position steps of tile j that hold positions
         const WinTile w = win_tile(tb, i0 + j, k);
         return (min(C::TP, w.end - w.start) + 15) / 16;
       };
-      auto issue_s = [&](int j) {
-        const int st = j % C::NK, b = j % C::NB;
-        const uint32_t id = umma_idesc_f16(C::M, 16 * steps(j, ks), false);
-        if (!mbar_wait(&k_full[st], (j / C::NK) & 1) ||
-            (j >= C::NB && !mbar_wait(&pv_done[b], ((j / C::NB) - 1) & 1)))
-          return false;
-        tc_fence_after();
-        const uint32_t sk = smem_addr(sK + st * C::KT);
-#pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-          for (int kk = 0; kk < C::KS_S; ++kk)
-            umma_f16(tbase + b * C::TP,
-                     umma_desc_sw128(q_addr + part * C::Q_PART + (kk >> 2) * C::Q_BOX + (kk & 3) * 32,
-                                     16, 1024),
-                     umma_desc_sw128(sk + (kk >> 2) * C::BOX + (kk & 3) * 32, 16, 1024), id,
-                     part + kk > 0 ? 1u : 0u);
-        umma_commit(&k_empty[st]);
-        umma_commit(&s_full[b]);
-        return true;
-      };
-      if (ok) ok = issue_s(0);
-      for (int j = 0; j < nt && ok; ++j) {
-        if (j + 1 < nt) ok = issue_s(j + 1);
-        const int st = j % C::NV, b = j % C::NB;
-        ok = ok && mbar_wait(&p_full[b], (j / C::NB) & 1) &&
-             mbar_wait(&v_full[st], (j / C::NV) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t sv = smem_addr(sV + st * C::KT);
-        const int nk = steps(j, ko);
-#pragma unroll 4
-        for (int kk = 0; kk < nk; ++kk)
+      if (is_s) {
+        const uint32_t q_addr = smem_addr(sQ);
+        for (int j = 0; j < nt && ok; ++j) {
+          const int st = j % C::NK, b = j % C::NB;
+          const uint32_t id = umma_idesc_f16(C::M, 16 * steps(j), false);
+          ok = (j < C::NB || mbar_wait(&pv_done[b], ((j / C::NB) - 1) & 1)) &&
+               mbar_wait(&k_full[st], (j / C::NK) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sk = smem_addr(sK + st * C::KT);
 #pragma unroll
           for (int part = 0; part < 2; ++part)
-            umma_f16_ta(tbase + C::O_COL, tbase + b * C::TP + part * (C::TP / 2) + kk * 8,
-                        umma_desc_sw128(sv + kk * 2048, C::BOX, 1024), kIdO,
-                        j + kk + part > 0 ? 1u : 0u);
-        umma_commit(&v_empty[st]);
-        umma_commit(&pv_done[b]);
+#pragma unroll
+            for (int kk = 0; kk < C::KS_S; ++kk)
+              umma_f16(tbase + b * C::TP,
+                       umma_desc_sw128(
+                           q_addr + part * C::Q_PART + (kk >> 2) * C::Q_BOX + (kk & 3) * 32, 16, 1024),
+                       umma_desc_sw128(sk + (kk >> 2) * C::BOX + (kk & 3) * 32, 16, 1024), id,
+                       part + kk > 0 ? 1u : 0u);
+          umma_commit(&s_full[b]);
+          umma_commit(&k_empty[st]);
+        }
+      } else {
+        constexpr uint32_t kIdO = umma_idesc_f16(C::M, D, true);
+        for (int j = 0; j < nt && ok; ++j) {
+          const int st = j % C::NV, b = j % C::NB;
+          const int nk = steps(j);
+          ok = mbar_wait(&v_full[st], (j / C::NV) & 1) && mbar_wait(&p_full[b], (j / C::NB) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sv = smem_addr(sV + st * C::KT);
+          const uint32_t pa = tbase + b * C::TP;
+#pragma unroll 4
+          for (int kk = 0; kk < nk; ++kk)
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+              umma_f16_ta(tbase + C::O_COL, pa + part * (C::TP / 2) + kk * 8,
+                          umma_desc_sw128(sv + kk * 2048, C::BOX, 1024), kIdO,
+                          j + kk + part > 0 ? 1u : 0u);
+          umma_commit(&pv_done[b]);
+          umma_commit(&v_empty[st]);
+        }
       }
-      umma_commit(drain);  // every MMA has completed before TMEM is freed
-      ok = mbar_wait(drain, 0) && ok;
+      umma_commit(&drain[is_s ? 0 : 1]);  // its MMAs have completed before TMEM is freed
+      ok = mbar_wait(&drain[is_s ? 0 : 1], 0) && ok;
       if (!ok) flag_error(p.err, GQA_ERR_TIMEOUT);
     }
     __syncwarp();
@@ -427,30 +458,9 @@ __global__ void __launch_bounds__(WinRowsCfg<D>::THREADS, 1)
     const int h = warp >> 2, i = threadIdx.x & 127;
     const int row = i / G;
     const bool rv = row < nr;
-    const int t = t0 + (rv ? row : 0), head = g * G + i % G;
     const Visible vis(rv ? tb.len[row] : 0, p.window, p.n_sink);
     const int run = rv ? tb.run[row] : -1;
     const uint32_t t_row = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    // q: fp32 pieces of 16 bytes to f16 hi and lo, 128-byte swizzled
-#pragma unroll 4
-    for (int f = threadIdx.x; f < C::M * (D / 4); f += 32 * C::NSW) {
-      const int qr = f / (D / 4), c4 = f % (D / 4), r = qr / G;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < nr)
-        x = __ldg(reinterpret_cast<const float4*>(
-                      p.q + ((size_t)(t0 + r) * p.n_heads + g * G + qr % G) * D) + c4);
-      uint2 hv, lv;
-      split_hi_lo(x.x * p.scale_log2, x.y * p.scale_log2, hv.x, lv.x);
-      split_hi_lo(x.z * p.scale_log2, x.w * p.scale_log2, hv.y, lv.y);
-      const int ch = c4 >> 1;
-      uint8_t* dst = sQ + (ch >> 3) * C::Q_BOX + qr * 128 + (((ch & 7) ^ (qr & 7)) << 4) +
-                     (c4 & 1) * 8;
-      *reinterpret_cast<uint2*>(dst) = hv;
-      *reinterpret_cast<uint2*>(dst + C::Q_PART) = lv;
-    }
-    fence_async_smem();
-    mbar_arrive(q_full);
-
     // After a wait has run out none is tried again, but every warp walks all tiles, so that the
     // barriers of the epilogue are met; the call flags GQA_ERR_TIMEOUT.
     bool ok = true;
@@ -558,28 +568,42 @@ __global__ void __launch_bounds__(WinRowsCfg<D>::THREADS, 1)
       mbar_arrive(&p_full[b]);
     }
 
-    // ---- O of the last tile, to the output or the chunk's partial: a half of the dims each
+    // ---- O of the last tile, to the output or the chunk's partial
     tb.mx[nt & 1][h][i] = l_run;
     named_bar_sync(2 + (warp & 3), 64);
     l_run += tb.mx[nt & 1][h ^ 1][i];
     wait(&pv_done[(nt - 1) % C::NB], ((nt - 1) / C::NB) & 1);
     tc_fence_after();
-    const WinOut<D> out(p, t, head, c, m_run, l_run);
-#pragma unroll 1
-    for (int q = 0; q < D / 64; ++q) {
-      const int d0 = h * (D / 2) + 32 * q;
-      uint32_t o[32];
-      tmem_ld32(t_row + C::O_COL + d0, o);
-      tmem_ld_landed(o);
-      if (rv) {
+    // through shared memory (the K/V rings, which nothing uses any more), so that a pair's row
+    // goes out as whole lines
+    constexpr int OS = D + 4;  // row stride in floats: 16-byte stores of 8 lanes on all banks
+    static_assert(C::M * OS * 4 <= C::Q_OFF, "O fits in the rings");
+    float* so = reinterpret_cast<float*>(sK) + i * OS + h * (D / 2);
 #pragma unroll
-        for (int e = 0; e < 32; e += 2)
-          *reinterpret_cast<float2*>(out.dst + d0 + e) =
-              make_float2(out.value(d0 + e, __uint_as_float(o[e])),
-                          out.value(d0 + e + 1, __uint_as_float(o[e + 1])));
-      }
+    for (int q = 0; q < D / 64; ++q) {
+      uint32_t o[32];
+      tmem_ld32(t_row + C::O_COL + h * (D / 2) + 32 * q, o);
+      tmem_ld_landed(o);
+#pragma unroll
+      for (int e = 0; e < 32; e += 4)
+        *reinterpret_cast<uint4*>(so + 32 * q + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
     }
-    if (rv && h == 0) out.stats();
+    if (h == 0) {
+      tb.m[i] = m_run;
+      tb.l[i] = l_run;
+    }
+    named_bar_sync(1, 32 * C::NSW);
+    for (int pair = warp; pair < nr * G; pair += C::NSW) {
+      const WinOut<D> out(p, t0 + pair / G, g * G + pair % G, c, tb.m[pair], tb.l[pair]);
+      const float2* src = reinterpret_cast<const float2*>(reinterpret_cast<float*>(sK) + pair * OS);
+#pragma unroll
+      for (int q = 0; q < D / 64; ++q) {
+        const int d = 2 * (lane + 32 * q);
+        const float2 x = src[lane + 32 * q];
+        *reinterpret_cast<float2*>(out.dst + d) = make_float2(out.value(d, x.x), out.value(d + 1, x.y));
+      }
+      if (lane == 0) out.stats();
+    }
     if (!ok && lane == 0) flag_error(p.err, GQA_ERR_TIMEOUT);
     named_bar_sync(1, 32 * C::NSW);
     if (tb.dirty) rows_plain<D>(p, tb, t0, nr, g, c, i0, i1, warp, lane);
