@@ -33,13 +33,16 @@ struct VisibleTiles {
 };
 
 // The 4-bit kernel's arguments: base.kc, vc, ksc, vsc hold the cache's pointers, base.window and
-// n_sink what a row sees, base.chunk counts tiles.
+// n_sink what a row sees, base.chunk counts tiles, base.counters hold a word per (group, grid.y).
 struct Q4Params {
   PartialParams base;
+  int rows;  // rows of a group: their (row, head) pairs are at most 8
   float k_scale, v_scale;
 };
 
-constexpr int kQ4Tile = 32;        // positions of a tile of the 4-bit kernel
+// positions of a tile of the 4-bit kernel: a warp's copies of 9 KB (D = 64: 4.6)
+__host__ __device__ constexpr int q4_tile(int head_dim) { return head_dim == 256 ? 32 : 64; }
+constexpr int kQ4MaxSplit = 1024;  // chunks of a row at most
 constexpr int kWinRowsTile = 128;  // ... of the kernel for rows that share a sequence
 
 // Row t's length and sequence; values out of range are flagged (by the thread that `flag` names)

@@ -65,10 +65,13 @@ gqa_status plan_visible(int n_tok, int n_seq, int n_heads, int n_kv_heads, int h
   }
   int hs = 1;  // 4-bit: CTAs of a KV head's query heads, at most 8 each
   while (q4 && (group % hs || group / hs > 8)) ++hs;
-  const int tile = q4 ? kQ4Tile : stage_rows(GQA_KIND_F16, head_dim);
+  const int tile = q4 ? q4_tile(head_dim) : stage_rows(GQA_KIND_F16, head_dim);
   // the sinks' last tile and the window's last one (4-bit: its first one too) are partly seen
   const long long tiles = (n + tile - 1) / tile + (budget > 0 ? 2 : 0);
-  const long long units = std::max(1LL, (long long)n_tok * n_kv_heads * hs);
+  // 4-bit rows that may share a sequence: as many a CTA as their heads leave room for
+  const int rows = q4 && n_seq < n_tok ? 8 / (group / hs) : 1;
+  const long long groups = (n_tok + rows - 1) / rows;
+  const long long units = std::max(1LL, groups * n_kv_heads * hs);
   const long long slots = (long long)(q4 ? kQ4CtasPerSm : kWinCtasPerSm) * num_sms;
   long long chunk = (units * tiles + slots - 1) / slots;
   chunk = std::max<long long>(chunk, q4 ? kQ4MinChunk / tile : kWinMinStages);
@@ -82,6 +85,7 @@ gqa_status plan_visible(int n_tok, int n_seq, int n_heads, int n_kv_heads, int h
     const long long c8 = (tiles + 7) / 8;
     if (units * ((tiles + c8 - 1) / c8) <= num_sms) chunk = c8;
   }
+  if (q4) chunk = std::max(chunk, (tiles + kQ4MaxSplit - 1) / kQ4MaxSplit);
   chunk = std::min(chunk, std::max(tiles, 1LL));
   const long long n_split = std::max(1LL, (tiles + chunk - 1) / chunk);
   if (n_split > (1 << 30) || (long long)n_kv_heads * hs > 65535)
@@ -91,7 +95,8 @@ gqa_status plan_visible(int n_tok, int n_seq, int n_heads, int n_kv_heads, int h
   plan->tile = tile;
   plan->grid_x = (int)n_split;
   plan->grid_y = n_kv_heads * hs;
-  plan->grid_z = n_tok;
+  plan->grid_z = (int)groups;
+  plan->row_group = rows;
   plan->merge = n_split > 1 ? 1 : 0;
   if (plan->merge) {
     const size_t cnt = ((size_t)n_tok * plan->grid_y * sizeof(uint32_t) + 255) / 256 * 256;
@@ -168,7 +173,7 @@ static gqa_status visible_common(int kind, const float* q, const void* kc, const
   p.scale_log2 = scale * 1.4426950408889634f;
   p.merge = plan.merge;
   p.head_split = std::max(1, plan.grid_y / n_kv_heads);
-  if (plan.merge && plan.row_group > 1) {  // ws = [partials][n_valid]
+  if (plan.merge && !q4 && plan.row_group > 1) {  // ws = [partials][n_valid]
     const size_t part = (size_t)n_tok * plan.n_split * n_heads * (head_dim + 2) * sizeof(float);
     p.part = static_cast<float*>(ws);
     p.n_valid = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + (part + 255) / 256 * 256);
@@ -185,6 +190,7 @@ static gqa_status visible_common(int kind, const float* q, const void* kc, const
   const dim3 grid(plan.grid_x, plan.grid_y, plan.grid_z);
   cudaError_t e;
   if (q4) {
+    qp.rows = plan.row_group;
     qp.k_scale = k_scale;
     qp.v_scale = v_scale;
     e = launch_q4(head_dim, qp, grid, stream);
