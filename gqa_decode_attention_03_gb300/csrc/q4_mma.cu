@@ -10,21 +10,23 @@
 // fill the 8 rows of the products that a row's heads leave empty: their tiles are those of the
 // union of what the rows see, sequence by sequence, and each pair masks its own.
 //
-// Both products run as mma.sync m16n8k16 with fp32 sums.  A = up to 8 pairs, their f16 hi
-// part in rows 0-7 and the f16 remainder in rows 8-15 (22 bits of q and of the softmax weights);
-// B = cache values, exact in f16 (q4_common.cuh): one conversion makes two codes f16x2 and one
-// f16x2 product applies their scales.
+// Both products run as mma.sync m16n8k16 with fp32 sums and the cache as A: its values are exact in
+// f16 (q4_common.cuh), one conversion makes two codes f16x2 and one f16x2 product applies their
+// scales.  B = four pairs, each as an f16 hi column and the column of its f16 remainder (22 bits of
+// q and of the softmax weights); PN such column blocks.  Codes as B and pairs as 16 rows took twice
+// the products for up to four pairs: 251 us against 184 for 57 rows of 16384 (D = 128, 4 heads).
 //
 // Fragments.  The dims and positions that a fragment's indices stand for are chosen so that a
 // thread's codes are contiguous (lane = 4 g + t):
-//   q.k  k index: thread t holds dims of its own 16-byte run of a position's codes, words w and
-//        bytes in order; q's A fragments are laid out alike.  n index: column n of n-tile nt is
-//        position 8 nt + 4 (n & 1) + ((n >> 1) ^ 3 (n & 1)).
-//   p.v  k index: the same positions, so the weights go from C to A layout in place; thread t's
-//        four are 4 j + (t ^ 3 (j & 1)), j = 0..3: for every j the four t read different banks as
-//        far as rows of 32 or 64 bytes allow.  n index: column n of n-tile i is dim n D/8 + i, so
-//        a thread's codes of a position are one run of D/16 bytes, and at D = 128 one scale.
-//        Two positions' codes are interleaved nibble by nibble before the conversion.
+//   k.q  row r of a 16-position block is position 8 (r >> 3) + 4 (r & 1) + ((r >> 1) & 3 ^ 3 (r & 1));
+//        thread t holds the dims of its own 16-byte run of a position's codes, word by word.  The
+//        result has pair t's hi and lo sums of positions g and g + 8 in a thread.
+//   v.p  k index: the same positions.  The weights go from that result to B by one movmatrix
+//        (a transposed 8 x 8 of f16) per 8 positions, hi and lo of a weight being one register.
+//        Rows g and g + 8 of m-tile i are dims g D/8 + 2 i and the next: a thread's codes of a
+//        position are one run of D/16 bytes, at D = 128 under one scale.  Two positions' codes are
+//        interleaved nibble by nibble before the conversion.
+// Rows of 32 or 64 bytes are read without bank conflicts in k.q and two at a time at most in v.p.
 #include "dispatch.h"
 #include "q4_common.cuh"
 #include "umma.cuh"
@@ -33,32 +35,33 @@
 
 namespace gqa {
 
-template <int D>
+template <int D, int PN_>
 struct Q4Cfg {
+  static constexpr int PN = PN_, NP = 4 * PN;       // column blocks, pairs
   static constexpr int NW = 4;                      // warps
   static constexpr int RB = D / 2, SB = D / 16;     // bytes of a position's codes and scales
   static constexpr int TP = q4_tile(D);             // positions of a tile, worked on SP at a time
-  static constexpr int SP = 32, NB = SP / 16, NTK = SP / 8;  // 16-position blocks, n-tiles of q.k
+  static constexpr int SP = 32, NB = SP / 16;       // 16-position blocks
   static constexpr int STAGE = 2 * TP * (RB + SB);  // [K codes][V codes][K scales][V scales]
   static constexpr int NST = D == 64 ? 4 : 2;
   static constexpr int MIN_CTAS = D == 256 ? 2 : 3;
-  static constexpr int KS = D / 16;                 // k-steps of q.k
+  static constexpr int KS = D / 16;                 // k-steps of k.q
   static constexpr int KW = D / 32;                 // words of a thread's codes of a K position
   static constexpr int VW = D / 64;                 // ... of a V position
-  static constexpr int NT = D / 8;                  // n-tiles of p.v
-  static constexpr bool QSMEM = D == 256;           // q's fragments stay in shared memory
+  static constexpr int MT = D / 16;                 // m-tiles of v.p
+  static constexpr bool QSMEM = D == 256 && PN > 1;  // q's fragments stay in shared memory
   static constexpr int RING = NW * NST * STAGE;
-  static constexpr int MERGE = NW * 8 * (D + 2) * 4;  // the warps' states, over the rings
+  static constexpr int MERGE = NW * NP * (D + 2) * 4;  // the warps' states, over the rings
   // q's fragments: in a place of their own, or (then read into registers) in warp 0's last stage
   // before it takes its first tile
-  static constexpr int QF_BYTES = KS * 32 * 16;
+  static constexpr int QF_BYTES = PN * KS * 32 * 8;
   static constexpr int QF_OFF = QSMEM ? RING : (NST - 1) * STAGE;
   static constexpr int NST0 = QSMEM ? NST : NST - 1;  // tiles asked for before q is in
   static constexpr int BAR_OFF = RING + (QSMEM ? QF_BYTES : 0);
   static constexpr int SMEM = BAR_OFF + NW * NST * 8;
   static_assert(QSMEM || QF_BYTES <= STAGE, "q's fragments fit a stage");
   static_assert(MIN_CTAS * (SMEM + 2304 + 1024) <= 228 * 1024, "MIN_CTAS fit an SM");
-  static_assert(MERGE <= RING && 8 * kQ4MaxSplit * 4 <= RING, "merge areas inside the rings");
+  static_assert(MERGE <= RING && NP * kQ4MaxSplit * 4 <= RING, "merge areas inside the rings");
   static constexpr float RESCALE_LOG2 = 8.f;
 };
 
@@ -101,20 +104,27 @@ struct Q4Walk {
   }
 };
 
-template <int D>
-__global__ void __launch_bounds__(32 * Q4Cfg<D>::NW, Q4Cfg<D>::MIN_CTAS)
+// An 8 x 8 matrix of f16, row lane / 4, columns 2 (lane % 4) and the next in a register: transposed.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+template <int D, int PN>
+__global__ void __launch_bounds__(32 * Q4Cfg<D, PN>::NW, Q4Cfg<D, PN>::MIN_CTAS)
     q4_mma_kernel(const Q4Params qp) {
-  using C = Q4Cfg<D>;
+  using C = Q4Cfg<D, PN>;
   extern __shared__ __align__(128) uint8_t smem[];
   const PartialParams& p = qp.base;
   __shared__ Q4Run s_runs[C::NW][9];
-  __shared__ float s_amax[C::NW][8];
+  __shared__ float s_amax[C::NW][C::NP];
   const int c = blockIdx.x;
   const int kvh = blockIdx.y / p.head_split;
   const int G = p.group / p.head_split;  // query heads of this CTA (<= 8)
   const int head0 = kvh * p.group + (blockIdx.y % p.head_split) * G;
   const int t0 = blockIdx.z * qp.rows, nr = min(qp.rows, p.n_tok - t0);
-  const int np = nr * G;                 // pairs: row gid / G, head gid % G
+  const int np = nr * G;                 // pairs (<= 4 PN): row i / G, head i % G
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -125,8 +135,14 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D>::NW, Q4Cfg<D>::MIN_CTAS)
   int seq = 0, len = 0;
   if (lane < nr)
     len = visible_row(p, t0 + lane, c == 0 && blockIdx.y == 0 && warp == 0, seq);
-  const int prow = gid < np ? gid / G : 0;
-  int prun = -1, nruns = 0, n = 0;
+  // this thread's pairs in scores and sums: 4 pn + tig
+  int prow[PN], prun[PN];
+#pragma unroll
+  for (int pn = 0; pn < PN; ++pn) {
+    prow[pn] = 4 * pn + tig < np ? (4 * pn + tig) / G : 0;
+    prun[pn] = -1;
+  }
+  int nruns = 0, n = 0;
   {
     Q4Run r{};
     auto close = [&] {
@@ -150,12 +166,21 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D>::NW, Q4Cfg<D>::MIN_CTAS)
         r.ns = max(r.ns, v.ns);
         r.end = max(r.end, v.L);
       }
-      if (k == prow) prun = nruns - 1;
+#pragma unroll
+      for (int pn = 0; pn < PN; ++pn)
+        if (k == prow[pn]) prun[pn] = nruns - 1;
     }
     if (nruns) close();
     if (lane == 0) runs[nruns].tiles0 = n;
   }
-  const Visible vis(__shfl_sync(0xffffffffu, len, prow), p.window, p.n_sink);
+  int vL[PN], vw0[PN], vns[PN];  // what the pairs' rows see
+#pragma unroll
+  for (int pn = 0; pn < PN; ++pn) {
+    const Visible v(__shfl_sync(0xffffffffu, len, prow[pn]), p.window, p.n_sink);
+    vL[pn] = v.L;
+    vw0[pn] = v.w0;
+    vns[pn] = v.ns;
+  }
   // p.chunk tiles a chunk, more where the rows of a group see so different positions that the
   // grid's chunks would not reach
   const int per = max(p.chunk, (n + p.n_split - 1) / p.n_split);
@@ -198,64 +223,82 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D>::NW, Q4Cfg<D>::MIN_CTAS)
   int issued = 0;  // the warp's tiles asked for so far
   for (int i = i0; issued < C::NST0 && i < i1; i += C::NW, ++issued) issue(i, issued);
 
-  // ---- q's A fragments: the pair's row scaled by a power of two to [1, 2) as f16 hi + lo; sm
+  // ---- q's B fragments: the pair's row scaled by a power of two to [1, 2) as f16 hi or lo; sm
   //      takes the power, the softmax scale and the cache's scale of K back in.  Each warp makes
-  //      those of its quarter of the k-steps.
-  uint4* qf = reinterpret_cast<uint4*>(smem + C::QF_OFF) + lane;
-  float sm;
+  //      those of its quarter of the k-steps: pair 4 pn + gid / 2, part gid & 1.
+  uint2* qf = reinterpret_cast<uint2*>(smem + C::QF_OFF) + lane;
+  float sm[PN];
   {
     constexpr int KW = C::KS / C::NW;
-    const bool hv = gid < np;
-    const float* qrow = p.q + ((size_t)(t0 + prow) * p.n_heads + head0 + (hv ? gid % G : 0)) * D;
-    float4 x[KW];
-    float amax = 0.f;
+    float4 x[PN][KW];
 #pragma unroll
-    for (int e = 0; e < KW; ++e) {
-      const int ks = warp * KW + e, w = ks / 2;  // word of the thread's run of codes, half of it
-      const int d = (w / 4) * 128 + (D == 64 ? 16 : 32) * tig + 8 * (w % 4) + 4 * (ks & 1);
-      x[e] = hv ? __ldg(reinterpret_cast<const float4*>(qrow + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
-      amax = fmaxf(amax, fmaxf(fmaxf(fabsf(x[e].x), fabsf(x[e].y)),
-                               fmaxf(fabsf(x[e].z), fabsf(x[e].w))));
+    for (int pn = 0; pn < PN; ++pn) {
+      const int pair = 4 * pn + (gid >> 1);
+      const bool hv = pair < np;
+      const int row = hv ? pair / G : 0;
+      const float* qrow =
+          p.q + ((size_t)(t0 + row) * p.n_heads + head0 + (hv ? pair - row * G : 0)) * D;
+      float amax = 0.f;
+#pragma unroll
+      for (int e = 0; e < KW; ++e) {
+        const int ks = warp * KW + e, w = ks / 2;  // word of the thread's run of codes, half of it
+        const int d = (w / 4) * 128 + (D == 64 ? 16 : 32) * tig + 8 * (w % 4) + 4 * (ks & 1);
+        x[pn][e] =
+            hv ? __ldg(reinterpret_cast<const float4*>(qrow + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        amax = fmaxf(amax, fmaxf(fmaxf(fabsf(x[pn][e].x), fabsf(x[pn][e].y)),
+                                 fmaxf(fabsf(x[pn][e].z), fabsf(x[pn][e].w))));
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      if ((lane & 7) == 0) s_amax[warp][pair] = amax;
     }
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    if (tig == 0) s_amax[warp][gid] = amax;
     __syncthreads();
+    auto exponent = [&](int pair) {  // biased, of the pair's largest |q|
+      float m = 0.f;
 #pragma unroll
-    for (int w = 0; w < C::NW; ++w) amax = fmaxf(amax, s_amax[w][gid]);
-    const uint32_t e2 = min(max(__float_as_uint(amax) >> 23, 1u), 253u);
-    const float f = __uint_as_float((254u - e2) << 23);  // 2^(127 - e2)
-    sm = p.scale_log2 * qp.k_scale * __uint_as_float(e2 << 23);
+      for (int w = 0; w < C::NW; ++w) m = fmaxf(m, s_amax[w][pair]);
+      return min(max(__float_as_uint(m) >> 23, 1u), 253u);
+    };
 #pragma unroll
-    for (int e = 0; e < KW; ++e) {
-      uint32_t a[4];
-      split_hi_lo(x[e].x * f, x[e].y * f, a[0], a[1]);
-      split_hi_lo(x[e].z * f, x[e].w * f, a[2], a[3]);
-      qf[(warp * KW + e) * 32] = make_uint4(a[0], a[1], a[2], a[3]);
+    for (int pn = 0; pn < PN; ++pn) {
+      sm[pn] = p.scale_log2 * qp.k_scale * __uint_as_float(exponent(4 * pn + tig) << 23);
+      const float f = __uint_as_float((254u - exponent(4 * pn + (gid >> 1))) << 23);  // 2^(127 - e)
+#pragma unroll
+      for (int e = 0; e < KW; ++e) {
+        uint2 hv, lv;
+        split_hi_lo(x[pn][e].x * f, x[pn][e].y * f, hv.x, lv.x);
+        split_hi_lo(x[pn][e].z * f, x[pn][e].w * f, hv.y, lv.y);
+        qf[(pn * C::KS + warp * KW + e) * 32] = gid & 1 ? lv : hv;
+      }
     }
   }
   __syncthreads();
-  uint32_t qa[C::QSMEM ? 1 : C::KS][4];
+  uint2 qb[C::QSMEM ? 1 : PN][C::QSMEM ? 1 : C::KS];
   if constexpr (!C::QSMEM) {
 #pragma unroll
-    for (int ks = 0; ks < C::KS; ++ks) {
-      const uint4 a4 = qf[ks * 32];
-      qa[ks][0] = a4.x;
-      qa[ks][1] = a4.y;
-      qa[ks][2] = a4.z;
-      qa[ks][3] = a4.w;
-    }
+    for (int pn = 0; pn < PN; ++pn)
+#pragma unroll
+      for (int ks = 0; ks < C::KS; ++ks) qb[pn][ks] = qf[(pn * C::KS + ks) * 32];
     fence_async_smem();  // the copy below follows these accesses
     __syncthreads();
+  }
+  if constexpr (C::NST0 < C::NST) {
     const int i = i0 + C::NST0 * C::NW;
     if (i < i1) issue(i, issued++);
   }
 
-  float o[C::NT][4];
+  float o[PN][C::MT][4];  // pair 4 pn + tig: dims (2 i, 2 i + 1) of the thread's run x (hi, lo)
 #pragma unroll
-  for (int n = 0; n < C::NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-  float m_run = -INFINITY, l_run = 0.f;  // pair gid; l_run over this thread's positions
-  // this thread's rows of a 16-position block: K columns of both n-tiles, V positions
+  for (int pn = 0; pn < PN; ++pn)
+#pragma unroll
+    for (int i = 0; i < C::MT; ++i) o[pn][i][0] = o[pn][i][1] = o[pn][i][2] = o[pn][i][3] = 0.f;
+  float m_run[PN], l_run[PN];  // l_run over this thread's positions
+#pragma unroll
+  for (int pn = 0; pn < PN; ++pn) {
+    m_run[pn] = -INFINITY;
+    l_run[pn] = 0.f;
+  }
+  // this thread's position of an 8-position half block in scores
   const int krow = 4 * (gid & 1) + ((gid >> 1) ^ (3 * (gid & 1)));
   int done = 0;
   bool ok = true;
@@ -264,178 +307,204 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D>::NW, Q4Cfg<D>::MIN_CTAS)
     ok = __all_sync(0xffffffffu, mbar_wait(&full[st], (done / C::NST) & 1));
     if (!ok) break;
     const uint8_t* stage = ring + st * C::STAGE;
-    // rows of the tile that the pair sees: [lo, hi) and [0, ns); a pad pair takes any
+    // rows of the tile that the pairs see: [lo, hi) and [0, ns); a pad pair takes any
     int start, end;
     walk.tile(runs, i, start, end);
-    int hi = gid >= np ? C::TP : walk.k == prun ? min(vis.L, end) - start : 0;
-    int lo = gid >= np ? 0 : vis.w0 - start, ns = vis.ns - start;
-    const bool whole = __all_sync(0xffffffffu, hi >= C::TP && (lo <= 0 || ns >= C::TP));
+    int lo[PN], hi[PN], ns[PN];
+    bool whole = true;
+#pragma unroll
+    for (int pn = 0; pn < PN; ++pn) {
+      const bool pad = 4 * pn + tig >= np;
+      hi[pn] = pad ? C::TP : walk.k == prun[pn] ? min(vL[pn], end) - start : 0;
+      lo[pn] = pad ? 0 : vw0[pn] - start;
+      ns[pn] = vns[pn] - start;
+      whole = whole && hi[pn] >= C::TP && (lo[pn] <= 0 || ns[pn] >= C::TP);
+    }
+    whole = __all_sync(0xffffffffu, whole);
 #pragma unroll 1
-    for (int r0 = 0; r0 < C::TP && start + r0 < end; r0 += C::SP, hi -= C::SP, lo -= C::SP, ns -= C::SP) {
-    const uint8_t* sk = stage + r0 * C::RB;
-    const uint8_t* sv = sk + C::TP * C::RB;
-    const uint8_t* ssk = stage + 2 * C::TP * C::RB + r0 * C::SB;
-    const uint8_t* ssv = ssk + C::TP * C::SB;
-    // -- S = Q . K^T of 32 positions, four n-tiles
-    float sc[C::NTK][4];
+    for (int r0 = 0; r0 < C::TP && start + r0 < end; r0 += C::SP) {
+      const uint8_t* sk = stage + r0 * C::RB;
+      const uint8_t* sv = sk + C::TP * C::RB;
+      const uint8_t* ssk = stage + 2 * C::TP * C::RB + r0 * C::SB;
+      const uint8_t* ssv = ssk + C::TP * C::SB;
+      // -- S^T = K . Q^T of 32 positions, two m-tiles
+      constexpr int CH = PN == 1 ? 2 : 1;  // chains of products per result
+      float sc[C::NB][PN][CH][4];
 #pragma unroll
-    for (int nt = 0; nt < C::NTK; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+      for (int b = 0; b < C::NB; ++b)
 #pragma unroll
-    for (int k = 0; k < (C::KW + 3) / 4; ++k) {  // a thread's 16-byte runs of codes
-      constexpr int W = cmin(C::KW, 4);
-      uint32_t kw[C::NTK][W];
-      __half2 ks2[C::NTK][W / 2];  // one scale per two words, broadcast
+        for (int pn = 0; pn < PN; ++pn)
 #pragma unroll
-      for (int nt = 0; nt < C::NTK; ++nt) {
-        const int r = 8 * nt + krow;
-        if constexpr (D == 64) {
-          const uint2 u = *reinterpret_cast<const uint2*>(sk + r * C::RB + 8 * tig);
-          kw[nt][0] = u.x;
-          kw[nt][1] = u.y;
-          const uint32_t b0 = ssk[r * C::SB + tig];
-          ks2[nt][0] = e4m3x2_to_f16x2(b0 | b0 << 16);
-        } else {
-          const uint4 u = *reinterpret_cast<const uint4*>(sk + r * C::RB + 64 * k + 16 * tig);
-          kw[nt][0] = u.x;
-          kw[nt][1] = u.y;
-          kw[nt][2] = u.z;
-          kw[nt][3] = u.w;
-          const uint32_t b2 =
-              *reinterpret_cast<const uint16_t*>(ssk + r * C::SB + 8 * k + 2 * tig);
-          const __half2 h = e4m3x2_to_f16x2(__byte_perm(b2, 0, 0x4140));
-          ks2[nt][0] = __low2half2(h);
-          ks2[nt][1] = __high2half2(h);
+          for (int ch = 0; ch < CH; ++ch)
+            sc[b][pn][ch][0] = sc[b][pn][ch][1] = sc[b][pn][ch][2] = sc[b][pn][ch][3] = 0.f;
+#pragma unroll
+      for (int k = 0; k < (C::KW + 3) / 4; ++k) {  // a thread's 16-byte runs of codes
+        constexpr int W = cmin(C::KW, 4);
+        uint32_t kw[C::NB][2][W];
+        __half2 ks2[C::NB][2][W / 2];  // one scale per two words, broadcast
+#pragma unroll
+        for (int b = 0; b < C::NB; ++b)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int r = 16 * b + 8 * j + krow;
+            if constexpr (D == 64) {
+              const uint2 u = *reinterpret_cast<const uint2*>(sk + r * C::RB + 8 * tig);
+              kw[b][j][0] = u.x;
+              kw[b][j][1] = u.y;
+              const uint32_t b0 = ssk[r * C::SB + tig];
+              ks2[b][j][0] = e4m3x2_to_f16x2(b0 | b0 << 16);
+            } else {
+              const uint4 u = *reinterpret_cast<const uint4*>(sk + r * C::RB + 64 * k + 16 * tig);
+              kw[b][j][0] = u.x;
+              kw[b][j][1] = u.y;
+              kw[b][j][2] = u.z;
+              kw[b][j][3] = u.w;
+              const uint32_t b2 =
+                  *reinterpret_cast<const uint16_t*>(ssk + r * C::SB + 8 * k + 2 * tig);
+              const __half2 h = e4m3x2_to_f16x2(__byte_perm(b2, 0, 0x4140));
+              ks2[b][j][0] = __low2half2(h);
+              ks2[b][j][1] = __high2half2(h);
+            }
+          }
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          uint2 bq[PN][2];
+#pragma unroll
+          for (int pn = 0; pn < PN; ++pn)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int ks = 2 * (4 * k + w) + e;
+              if constexpr (C::QSMEM)
+                bq[pn][e] = qf[(pn * C::KS + ks) * 32];
+              else
+                bq[pn][e] = qb[pn][ks];
+            }
+#pragma unroll
+          for (int b = 0; b < C::NB; ++b) {
+            uint32_t h0[4], h1[4];
+            e2m1x8_to_f16x2(kw[b][0][w], h0);
+            e2m1x8_to_f16x2(kw[b][1][w], h1);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              h0[e] = mul_h2(h0[e], ks2[b][0][w / 2]);
+              h1[e] = mul_h2(h1[e], ks2[b][1][w / 2]);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t a[4] = {h0[2 * e], h1[2 * e], h0[2 * e + 1], h1[2 * e + 1]};
+#pragma unroll
+              for (int pn = 0; pn < PN; ++pn)
+                mma_f16(sc[b][pn][e % CH], a, bq[pn][e].x, bq[pn][e].y);
+            }
+          }
         }
       }
+      // -- the pairs' scores at positions 16 b + 8 j + krow, softmax weights, B fragments of P^T
+      uint32_t pb[PN][C::NB][2];
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        uint32_t a[2][4];
+      for (int pn = 0; pn < PN; ++pn) {
+        float x[C::NB][2];
+        float mt = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int ks = 2 * (4 * k + w) + e;
-          if constexpr (C::QSMEM) {
-            const uint4 a4 = qf[ks * 32];
-            a[e][0] = a4.x;
-            a[e][1] = a4.y;
-            a[e][2] = a4.z;
-            a[e][3] = a4.w;
+        for (int b = 0; b < C::NB; ++b)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float y = sc[b][pn][0][2 * j] + sc[b][pn][0][2 * j + 1];
+            if constexpr (CH == 2) y += sc[b][pn][1][2 * j] + sc[b][pn][1][2 * j + 1];
+            x[b][j] = y * sm[pn];
+            if (!whole) {
+              const int r = r0 + 16 * b + 8 * j + krow;
+              if (r >= hi[pn] || (r < lo[pn] && r >= ns[pn])) x[b][j] = -INFINITY;
+            }
+            mt = fmaxf(mt, x[b][j]);
+          }
+        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
+        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
+        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
+        // the running maximum moves only when 32 positions exceed it by 2^8 (weights <= 256)
+        const bool grow = mt > m_run[pn] + C::RESCALE_LOG2;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float m_new = grow ? mt : m_run[pn];
+          const float corr = m_run[pn] == -INFINITY ? 0.f : fast_exp2(m_run[pn] - m_new);
+          m_run[pn] = m_new;
+          l_run[pn] *= corr;
+#pragma unroll
+          for (int i2 = 0; i2 < C::MT; ++i2) {
+            o[pn][i2][0] *= corr;
+            o[pn][i2][1] *= corr;
+            o[pn][i2][2] *= corr;
+            o[pn][i2][3] *= corr;
+          }
+        }
+        const float mu = m_run[pn] == -INFINITY ? 0.f : m_run[pn];
+#pragma unroll
+        for (int b = 0; b < C::NB; ++b)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float w = fast_exp2(x[b][j] - mu);  // 0 where masked
+            l_run[pn] += w;
+            const float lw = w - __half2float(__float2half_rn(w));
+            pb[pn][b][j] = transpose_8x8(h2_bits(__floats2half2_rn(w, lw)));  // (hi, lo)
+          }
+      }
+      // -- O^T += V^T . P^T, 16 positions at a time.  Codes of a masked position are finite
+      //    whatever they hold, and weigh 0; so are those behind the positions that were copied.
+#pragma unroll
+      for (int b = 0; b < C::NB; ++b) {
+        uint32_t vw[4][C::VW];
+        uint32_t vs[4];  // scales: one byte, or two at D = 256
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = 16 * b + 4 * j + (tig ^ (3 * (j & 1)));
+          const uint8_t* src = sv + r * C::RB + gid * (D / 16);
+          if constexpr (D == 64) {
+            vw[j][0] = *reinterpret_cast<const uint32_t*>(src);
+            vs[j] = ssv[r * C::SB + gid / 2];
+          } else if constexpr (D == 128) {
+            const uint2 u = *reinterpret_cast<const uint2*>(src);
+            vw[j][0] = u.x;
+            vw[j][1] = u.y;
+            vs[j] = ssv[r * C::SB + gid];
           } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) a[e][i] = qa[ks][i];
+            const uint4 u = *reinterpret_cast<const uint4*>(src);
+            vw[j][0] = u.x;
+            vw[j][1] = u.y;
+            vw[j][2] = u.z;
+            vw[j][3] = u.w;
+            vs[j] = *reinterpret_cast<const uint16_t*>(ssv + r * C::SB + 2 * gid);
           }
         }
 #pragma unroll
-        for (int nt = 0; nt < C::NTK; ++nt) {
-          uint32_t h[4];
-          e2m1x8_to_f16x2(kw[nt][w], h);
+        for (int h = 0; h < (D == 256 ? 2 : 1); ++h) {  // scale groups of the thread's dims
+          __half2 s01, s23;
+          if constexpr (D == 256) {
+            s01 = e4m3x2_to_f16x2(__byte_perm(vs[0], vs[1], h ? 0x5511 : 0x4400));
+            s23 = e4m3x2_to_f16x2(__byte_perm(vs[2], vs[3], h ? 0x5511 : 0x4400));
+          } else {
+            s01 = e4m3x2_to_f16x2(vs[0] | vs[1] << 16);
+            s23 = e4m3x2_to_f16x2(vs[2] | vs[3] << 16);
+          }
+          constexpr int WG = D == 256 ? 2 : C::VW;  // words of the group
 #pragma unroll
-          for (int e = 0; e < 4; ++e) h[e] = mul_h2(h[e], ks2[nt][w / 2]);
-          mma_f16(sc[nt], a[0], h[0], h[1]);
-          mma_f16(sc[nt], a[1], h[2], h[3]);
-        }
-      }
-    }
-    // -- pair gid's scores at positions 8 nt + 4 j + (tig ^ 3 j)
-    float x[C::NTK][2];
-    float mt = -INFINITY;
+          for (int w = 0; w < WG; ++w) {
+            const int ww = WG * h + w;
+            constexpr uint32_t M = 0x0f0f0f0fu;
+            uint32_t e01[4], o01[4], e23[4], o23[4];  // even and odd dims of two positions
+            e2m1x8_to_f16x2((vw[0][ww] & M) | ((vw[1][ww] << 4) & ~M), e01);
+            e2m1x8_to_f16x2(((vw[0][ww] >> 4) & M) | (vw[1][ww] & ~M), o01);
+            e2m1x8_to_f16x2((vw[2][ww] & M) | ((vw[3][ww] << 4) & ~M), e23);
+            e2m1x8_to_f16x2(((vw[2][ww] >> 4) & M) | (vw[3][ww] & ~M), o23);
 #pragma unroll
-    for (int nt = 0; nt < C::NTK; ++nt)
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t a[4] = {mul_h2(e01[k], s01), mul_h2(o01[k], s01), mul_h2(e23[k], s23),
+                                     mul_h2(o23[k], s23)};
 #pragma unroll
-      for (int j = 0; j < 2; ++j) x[nt][j] = (sc[nt][j] + sc[nt][2 + j]) * sm;
-    if (!whole) {
-#pragma unroll
-      for (int nt = 0; nt < C::NTK; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int r = 8 * nt + 4 * j + (tig ^ (3 * j));
-          if (r >= hi || (r < lo && r >= ns)) x[nt][j] = -INFINITY;
-        }
-    }
-#pragma unroll
-    for (int nt = 0; nt < C::NTK; ++nt) mt = fmaxf(mt, fmaxf(x[nt][0], x[nt][1]));
-    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
-    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
-    // -- the running maximum moves only when a tile exceeds it by 2^8 (weights <= 256)
-    const bool grow = mt > m_run + C::RESCALE_LOG2;
-    if (__any_sync(0xffffffffu, grow)) {
-      const float m_new = grow ? mt : m_run;
-      const float corr = m_run == -INFINITY ? 0.f : fast_exp2(m_run - m_new);
-      m_run = m_new;
-      l_run *= corr;
-#pragma unroll
-      for (int n = 0; n < C::NT; ++n) {
-        o[n][0] *= corr;
-        o[n][1] *= corr;
-        o[n][2] *= corr;
-        o[n][3] *= corr;
-      }
-    }
-    const float mu = m_run == -INFINITY ? 0.f : m_run;
-#pragma unroll
-    for (int nt = 0; nt < C::NTK; ++nt)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        x[nt][j] = fast_exp2(x[nt][j] - mu);  // 0 where masked
-        l_run += x[nt][j];
-      }
-    // -- O += P . V, 16 positions at a time.  Codes of a masked position are finite whatever they
-    //    hold, and weigh 0; behind the positions that were copied the stage holds older codes.
-#pragma unroll
-    for (int b = 0; b < C::NB; ++b) {
-      uint32_t pa[4];
-      split_hi_lo(x[2 * b][0], x[2 * b][1], pa[0], pa[1]);
-      split_hi_lo(x[2 * b + 1][0], x[2 * b + 1][1], pa[2], pa[3]);
-      uint32_t vw[4][C::VW];
-      uint32_t vs[4];  // scales: one byte, or two at D = 256
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = 16 * b + 4 * j + (tig ^ (3 * (j & 1)));
-        const uint8_t* src = sv + r * C::RB + gid * (D / 16);
-        if constexpr (D == 64) {
-          vw[j][0] = *reinterpret_cast<const uint32_t*>(src);
-          vs[j] = ssv[r * C::SB + gid / 2];
-        } else if constexpr (D == 128) {
-          const uint2 u = *reinterpret_cast<const uint2*>(src);
-          vw[j][0] = u.x;
-          vw[j][1] = u.y;
-          vs[j] = ssv[r * C::SB + gid];
-        } else {
-          const uint4 u = *reinterpret_cast<const uint4*>(src);
-          vw[j][0] = u.x;
-          vw[j][1] = u.y;
-          vw[j][2] = u.z;
-          vw[j][3] = u.w;
-          vs[j] = *reinterpret_cast<const uint16_t*>(ssv + r * C::SB + 2 * gid);
-        }
-      }
-#pragma unroll
-      for (int h = 0; h < (D == 256 ? 2 : 1); ++h) {  // scale groups of the thread's dims
-        __half2 s01, s23;
-        if constexpr (D == 256) {
-          s01 = e4m3x2_to_f16x2(__byte_perm(vs[0], vs[1], h ? 0x5511 : 0x4400));
-          s23 = e4m3x2_to_f16x2(__byte_perm(vs[2], vs[3], h ? 0x5511 : 0x4400));
-        } else {
-          s01 = e4m3x2_to_f16x2(vs[0] | vs[1] << 16);
-          s23 = e4m3x2_to_f16x2(vs[2] | vs[3] << 16);
-        }
-        constexpr int WG = D == 256 ? 2 : C::VW;  // words of the group
-#pragma unroll
-        for (int w = 0; w < WG; ++w) {
-          const int ww = WG * h + w;
-          constexpr uint32_t M = 0x0f0f0f0fu;
-          uint32_t e01[4], o01[4], e23[4], o23[4];  // even and odd dims of two positions
-          e2m1x8_to_f16x2((vw[0][ww] & M) | ((vw[1][ww] << 4) & ~M), e01);
-          e2m1x8_to_f16x2(((vw[0][ww] >> 4) & M) | (vw[1][ww] & ~M), o01);
-          e2m1x8_to_f16x2((vw[2][ww] & M) | ((vw[3][ww] << 4) & ~M), e23);
-          e2m1x8_to_f16x2(((vw[2][ww] >> 4) & M) | (vw[3][ww] & ~M), o23);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            mma_f16(o[8 * ww + 2 * k], pa, mul_h2(e01[k], s01), mul_h2(e23[k], s23));
-            mma_f16(o[8 * ww + 2 * k + 1], pa, mul_h2(o01[k], s01), mul_h2(o23[k], s23));
+              for (int pn = 0; pn < PN; ++pn)
+                mma_f16(o[pn][4 * ww + k], a, pb[pn][b][0], pb[pn][b][1]);
+            }
           }
         }
       }
-    }
     }
     __syncwarp();  // every lane has read the stage
     const int nxt = i + C::NST * C::NW;
@@ -449,33 +518,35 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D>::NW, Q4Cfg<D>::MIN_CTAS)
     for (int k = done; k < issued; ++k)  // no copy may outlive the CTA
       (void)mbar_wait(&full[k % C::NST], (k / C::NST) & 1);
   }
-  l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
-  l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
-  keep_nan(m_run, l_run, o);
+#pragma unroll
+  for (int pn = 0; pn < PN; ++pn) {
+#pragma unroll
+    for (int x = 4; x < 32; x *= 2) l_run[pn] += __shfl_xor_sync(0xffffffffu, l_run[pn], x);
+    keep_nan(m_run[pn], l_run[pn], o[pn]);
+  }
 
   // ---- the four warps' states meet in shared memory (over the rings, which are drained)
   __syncthreads();
-  float* mg = reinterpret_cast<float*>(smem);  // [warp][8][D + 2]
-  float* mrow = mg + (warp * 8 + gid) * (D + 2);
+  float* mg = reinterpret_cast<float*>(smem);  // [warp][pair][D + 2]
 #pragma unroll
-  for (int n2 = 0; n2 < C::NT; ++n2) {
-    mrow[2 * tig * (D / 8) + n2] = o[n2][0] + o[n2][2];
-    mrow[(2 * tig + 1) * (D / 8) + n2] = o[n2][1] + o[n2][3];
+  for (int pn = 0; pn < PN; ++pn) {
+    float* mrow = mg + (warp * C::NP + 4 * pn + tig) * (D + 2);
+#pragma unroll
+    for (int i = 0; i < C::MT; ++i)
+      *reinterpret_cast<float2*>(mrow + gid * (D / 8) + 2 * i) =
+          make_float2(o[pn][i][0] + o[pn][i][1], o[pn][i][2] + o[pn][i][3]);
+    if (gid == 0) *reinterpret_cast<float2*>(mrow + D) = make_float2(m_run[pn], l_run[pn]);
   }
-  if (tig == 0) {
-    mrow[D] = m_run;
-    mrow[D + 1] = l_run;
-  }
-  __shared__ float s_w[C::NW][8], s_m[8], s_l[8];  // the warps' weights; the pair's maximum, sum
+  __shared__ float s_w[C::NW][C::NP], s_m[C::NP], s_l[C::NP];  // warps' weights; maximum and sum
   __syncthreads();
-  if (threadIdx.x < 8) {
+  if (threadIdx.x < C::NP) {
     const int h = threadIdx.x;
     float M = -INFINITY, Ls = 0.f;
 #pragma unroll
-    for (int w = 0; w < C::NW; ++w) M = fmaxf(M, mg[(w * 8 + h) * (D + 2) + D]);
+    for (int w = 0; w < C::NW; ++w) M = fmaxf(M, mg[(w * C::NP + h) * (D + 2) + D]);
 #pragma unroll
     for (int w = 0; w < C::NW; ++w) {
-      const float* r = mg + (w * 8 + h) * (D + 2);
+      const float* r = mg + (w * C::NP + h) * (D + 2);
       const float e = r[D] == -INFINITY ? 0.f : fast_exp2(r[D] - M);
       s_w[w][h] = e * qp.v_scale;
       Ls = fmaf(r[D + 1], e, Ls);
@@ -499,7 +570,7 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D>::NW, Q4Cfg<D>::MIN_CTAS)
       float2 a = make_float2(0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < C::NW; ++w) {
-        const float2 x = *reinterpret_cast<const float2*>(mg + (w * 8 + h) * (D + 2) + d);
+        const float2 x = *reinterpret_cast<const float2*>(mg + (w * C::NP + h) * (D + 2) + d);
         a.x = fmaf(x.x, e[w], a.x);
         a.y = fmaf(x.y, e[w], a.y);
       }
@@ -521,7 +592,7 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D>::NW, Q4Cfg<D>::MIN_CTAS)
   __syncthreads();
   if (!s_last) return;
   __threadfence();
-  float* wt = reinterpret_cast<float*>(smem);  // [8][nchunks]
+  float* wt = reinterpret_cast<float*>(smem);  // [pair][nchunks]
   for (int h = warp; h < np; h += C::NW) {
     const int row = h / G;
     const float* src =
@@ -568,10 +639,10 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D>::NW, Q4Cfg<D>::MIN_CTAS)
   }
 }
 
-template <int D>
+template <int D, int PN>
 static cudaError_t launch_q4_d(const Q4Params& qp, dim3 grid, cudaStream_t s) {
-  using C = Q4Cfg<D>;
-  const void* fn = reinterpret_cast<const void*>(&q4_mma_kernel<D>);
+  using C = Q4Cfg<D, PN>;
+  const void* fn = reinterpret_cast<const void*>(&q4_mma_kernel<D, PN>);
   cudaError_t e = ensure_smem(fn, C::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -582,13 +653,17 @@ static cudaError_t launch_q4_d(const Q4Params& qp, dim3 grid, cudaStream_t s) {
   cudaLaunchAttribute at[2];
   cfg.attrs = at;
   cfg.numAttrs = cluster_attrs(at, 0, 1);
-  return cudaLaunchKernelEx(&cfg, &q4_mma_kernel<D>, qp);
+  return cudaLaunchKernelEx(&cfg, &q4_mma_kernel<D, PN>, qp);
 }
 
 cudaError_t launch_q4(int head_dim, const Q4Params& qp, dim3 grid, cudaStream_t s) {
-  if (head_dim == 64) return launch_q4_d<64>(qp, grid, s);
-  if (head_dim == 128) return launch_q4_d<128>(qp, grid, s);
-  return launch_q4_d<256>(qp, grid, s);
+  // a CTA's pairs, at most 8, in one block of four columns or two
+  const int np = qp.rows * (qp.base.group / qp.base.head_split);
+  if (head_dim == 64)
+    return np <= 4 ? launch_q4_d<64, 1>(qp, grid, s) : launch_q4_d<64, 2>(qp, grid, s);
+  if (head_dim == 128)
+    return np <= 4 ? launch_q4_d<128, 1>(qp, grid, s) : launch_q4_d<128, 2>(qp, grid, s);
+  return np <= 4 ? launch_q4_d<256, 1>(qp, grid, s) : launch_q4_d<256, 2>(qp, grid, s);
 }
 
 }  // namespace gqa
