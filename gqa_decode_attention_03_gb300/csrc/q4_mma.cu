@@ -1,8 +1,10 @@
 // q4_mma.cu -- decode attention over the 4-bit cache on the tensor cores.
 //
-// One CTA per (chunk of visible tiles, KV head x head split, group of rows); each of its four warps
-// streams every fourth tile of the chunk through a ring of its own and keeps its own running
-// maximum, sum and accumulator, so nothing but the end of the chunk synchronises the CTA.  A tile
+// A CTA works on a piece of the list of tiles that a (group of rows, KV head x head split) sees: a
+// chunk of it, one a CTA, or, where that would take several waves of long chunks, an equal share of
+// all lists end to end (the 16-row ragged batch: 63.4 us against 69.8).  Each of its four warps
+// streams every fourth tile of the piece through a ring of its own and keeps its own running
+// maximum, sum and accumulator, so nothing but the end of the piece synchronises the CTA.  A tile
 // is TP positions of one KV head: four contiguous runs of the head-major cache (codes and scales of
 // K and of V), which the warp's first lane copies with cp.async.bulk; the ring holds NST tiles.
 //
@@ -44,7 +46,7 @@ struct Q4Cfg {
   static constexpr int SP = 32, NB = SP / 16;       // 16-position blocks
   static constexpr int STAGE = 2 * TP * (RB + SB);  // [K codes][V codes][K scales][V scales]
   static constexpr int NST = D == 64 ? 4 : 2;
-  static constexpr int MIN_CTAS = D == 256 ? 2 : 3;
+  static constexpr int MIN_CTAS = q4_ctas_per_sm(D, PN);
   static constexpr int KS = D / 16;                 // k-steps of k.q
   static constexpr int KW = D / 32;                 // words of a thread's codes of a K position
   static constexpr int VW = D / 64;                 // ... of a V position
@@ -111,30 +113,52 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   return r;
 }
 
+// What a CTA works on at a time: tiles [a, b) of a (group z, column y) -- all of its pieces are
+// merged by the CTA that finishes last.
+struct Q4Item {
+  int z, y;             // group of rows; KV head x head split
+  int a, b;             // its tiles (b < 0: chunk `piece` of the grid's cut)
+  int piece, pieces;    // this piece and their number (b < 0: found from the list's length)
+  int slot;             // balanced: record slot of piece 0's CTA
+};
+
 template <int D, int PN>
-__global__ void __launch_bounds__(32 * Q4Cfg<D, PN>::NW, Q4Cfg<D, PN>::MIN_CTAS)
-    q4_mma_kernel(const Q4Params qp) {
+__device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const Q4Item& it,
+                                        uint32_t& phases) {
   using C = Q4Cfg<D, PN>;
-  extern __shared__ __align__(128) uint8_t smem[];
   const PartialParams& p = qp.base;
   __shared__ Q4Run s_runs[C::NW][9];
   __shared__ float s_amax[C::NW][C::NP];
-  const int c = blockIdx.x;
-  const int kvh = blockIdx.y / p.head_split;
+  const int kvh = it.y / p.head_split;
   const int G = p.group / p.head_split;  // query heads of this CTA (<= 8)
-  const int head0 = kvh * p.group + (blockIdx.y % p.head_split) * G;
-  const int t0 = blockIdx.z * qp.rows, nr = min(qp.rows, p.n_tok - t0);
+  const int head0 = kvh * p.group + (it.y % p.head_split) * G;
+  const int t0 = it.z * qp.rows, nr = min(qp.rows, p.n_tok - t0);
   const int np = nr * G;                 // pairs (<= 4 PN): row i / G, head i % G
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
+
+  // this warp's quarter of q, asked for before anything else is known: pair 4 pn + gid / 2
+  constexpr int QW = C::KS / C::NW;
+  float4 qx[PN][QW];
+#pragma unroll
+  for (int pn = 0; pn < PN; ++pn) {
+    const int pair = 4 * pn + (gid >> 1), row = pair < np ? pair / G : 0;
+    const float* qrow =
+        p.q + ((size_t)(t0 + row) * p.n_heads + head0 + (pair < np ? pair - row * G : 0)) * D;
+#pragma unroll
+    for (int e = 0; e < QW; ++e) {
+      const int ks = warp * QW + e, w = ks / 2;  // word of the thread's run of codes, half of it
+      const int d = (w / 4) * 128 + (D == 64 ? 16 : 32) * tig + 8 * (w % 4) + 4 * (ks & 1);
+      qx[pn][e] = pair < np ? __ldg(reinterpret_cast<const float4*>(qrow + d))
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
 
   // ---- the rows (lane k: row k), their runs (every warp its own table) and this pair's row
   Q4Run* runs = s_runs[warp];
   int seq = 0, len = 0;
   if (lane < nr)
-    len = visible_row(p, t0 + lane, c == 0 && blockIdx.y == 0 && warp == 0, seq);
+    len = visible_row(p, t0 + lane, it.y == 0 && it.piece == 0 && warp == 0, seq);
   // this thread's pairs in scores and sums: 4 pn + tig
   int prow[PN], prun[PN];
 #pragma unroll
@@ -181,17 +205,21 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D, PN>::NW, Q4Cfg<D, PN>::MIN_CTAS)
     vw0[pn] = v.w0;
     vns[pn] = v.ns;
   }
-  // p.chunk tiles a chunk, more where the rows of a group see so different positions that the
-  // grid's chunks would not reach
-  const int per = max(p.chunk, (n + p.n_split - 1) / p.n_split);
-  const int nchunks = (n + per - 1) / per;
-  if (c >= nchunks) {
-    if (c == 0)  // nothing to see: zeros
-      for (int i = threadIdx.x; i < np * D; i += blockDim.x)
-        p.out[((size_t)(t0 + i / (G * D)) * p.n_heads + head0) * D + i % (G * D)] = 0.f;
-    return;
+  int first = it.a, last = it.b, pieces = it.pieces;
+  if (it.b < 0) {  // p.chunk tiles a chunk, more where the rows of a group see so different
+                   // positions that the grid's chunks would not reach
+    const int per = max(p.chunk, (n + p.n_split - 1) / p.n_split);
+    pieces = (n + per - 1) / per;
+    first = it.piece * per;
+    last = min(first + per, n);
+    if (first >= n) {
+      if (it.piece == 0)  // nothing to see: zeros
+        for (int i = threadIdx.x; i < np * D; i += blockDim.x)
+          p.out[((size_t)(t0 + i / (G * D)) * p.n_heads + head0) * D + i % (G * D)] = 0.f;
+      return;
+    }
   }
-  const int i0 = c * per + warp, i1 = min((c + 1) * per, n);
+  const int i0 = first + warp, i1 = last;
 
   uint8_t* ring = smem + warp * C::NST * C::STAGE;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF) + warp * C::NST;
@@ -215,11 +243,6 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D, PN>::NW, Q4Cfg<D, PN>::MIN_CTAS)
     bulk_load(dst + C::TP * C::SB, reinterpret_cast<const uint8_t*>(p.vsc) + row * C::SB,
               m * C::SB, &full[st]);
   };
-  if (lane == 0) {
-    for (int st = 0; st < C::NST; ++st) mbar_init(&full[st], 1);
-    mbar_init_fence();
-  }
-  __syncwarp();  // the barriers, before any lane waits on one
   int issued = 0;  // the warp's tiles asked for so far
   for (int i = i0; issued < C::NST0 && i < i1; i += C::NW, ++issued) issue(i, issued);
 
@@ -229,28 +252,16 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D, PN>::NW, Q4Cfg<D, PN>::MIN_CTAS)
   uint2* qf = reinterpret_cast<uint2*>(smem + C::QF_OFF) + lane;
   float sm[PN];
   {
-    constexpr int KW = C::KS / C::NW;
-    float4 x[PN][KW];
 #pragma unroll
     for (int pn = 0; pn < PN; ++pn) {
-      const int pair = 4 * pn + (gid >> 1);
-      const bool hv = pair < np;
-      const int row = hv ? pair / G : 0;
-      const float* qrow =
-          p.q + ((size_t)(t0 + row) * p.n_heads + head0 + (hv ? pair - row * G : 0)) * D;
       float amax = 0.f;
 #pragma unroll
-      for (int e = 0; e < KW; ++e) {
-        const int ks = warp * KW + e, w = ks / 2;  // word of the thread's run of codes, half of it
-        const int d = (w / 4) * 128 + (D == 64 ? 16 : 32) * tig + 8 * (w % 4) + 4 * (ks & 1);
-        x[pn][e] =
-            hv ? __ldg(reinterpret_cast<const float4*>(qrow + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
-        amax = fmaxf(amax, fmaxf(fmaxf(fabsf(x[pn][e].x), fabsf(x[pn][e].y)),
-                                 fmaxf(fabsf(x[pn][e].z), fabsf(x[pn][e].w))));
-      }
+      for (int e = 0; e < QW; ++e)
+        amax = fmaxf(amax, fmaxf(fmaxf(fabsf(qx[pn][e].x), fabsf(qx[pn][e].y)),
+                                 fmaxf(fabsf(qx[pn][e].z), fabsf(qx[pn][e].w))));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      if ((lane & 7) == 0) s_amax[warp][pair] = amax;
+      if ((lane & 7) == 0) s_amax[warp][4 * pn + (gid >> 1)] = amax;
     }
     __syncthreads();
     auto exponent = [&](int pair) {  // biased, of the pair's largest |q|
@@ -264,11 +275,11 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D, PN>::NW, Q4Cfg<D, PN>::MIN_CTAS)
       sm[pn] = p.scale_log2 * qp.k_scale * __uint_as_float(exponent(4 * pn + tig) << 23);
       const float f = __uint_as_float((254u - exponent(4 * pn + (gid >> 1))) << 23);  // 2^(127 - e)
 #pragma unroll
-      for (int e = 0; e < KW; ++e) {
+      for (int e = 0; e < QW; ++e) {
         uint2 hv, lv;
-        split_hi_lo(x[pn][e].x * f, x[pn][e].y * f, hv.x, lv.x);
-        split_hi_lo(x[pn][e].z * f, x[pn][e].w * f, hv.y, lv.y);
-        qf[(pn * C::KS + warp * KW + e) * 32] = gid & 1 ? lv : hv;
+        split_hi_lo(qx[pn][e].x * f, qx[pn][e].y * f, hv.x, lv.x);
+        split_hi_lo(qx[pn][e].z * f, qx[pn][e].w * f, hv.y, lv.y);
+        qf[(pn * C::KS + warp * QW + e) * 32] = gid & 1 ? lv : hv;
       }
     }
   }
@@ -304,8 +315,9 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D, PN>::NW, Q4Cfg<D, PN>::MIN_CTAS)
   bool ok = true;
   for (int i = i0; i < i1; i += C::NW, ++done) {
     const int st = done % C::NST;
-    ok = __all_sync(0xffffffffu, mbar_wait(&full[st], (done / C::NST) & 1));
+    ok = __all_sync(0xffffffffu, mbar_wait(&full[st], (phases >> st) & 1));
     if (!ok) break;
+    phases ^= 1u << st;
     const uint8_t* stage = ring + st * C::STAGE;
     // rows of the tile that the pairs see: [lo, hi) and [0, ns); a pad pair takes any
     int start, end;
@@ -515,8 +527,10 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D, PN>::NW, Q4Cfg<D, PN>::MIN_CTAS)
   }
   if (!ok) {
     if (lane == 0) flag_error(p.err, GQA_ERR_TIMEOUT);
-    for (int k = done; k < issued; ++k)  // no copy may outlive the CTA
-      (void)mbar_wait(&full[k % C::NST], (k / C::NST) & 1);
+    for (int k = done; k < issued; ++k) {  // no copy may outlive the CTA
+      (void)mbar_wait(&full[k % C::NST], (phases >> (k % C::NST)) & 1);
+      phases ^= 1u << (k % C::NST);
+    }
   }
 #pragma unroll
   for (int pn = 0; pn < PN; ++pn) {
@@ -555,12 +569,21 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D, PN>::NW, Q4Cfg<D, PN>::MIN_CTAS)
     s_l[h] = Ls;
   }
   __syncthreads();
-  const bool split = nchunks > 1;
-  const size_t rec = (size_t)p.n_heads * (D + 2);  // floats between a pair's chunks
+  const bool split = pieces > 1;
+  // Records [D + 2] of a pair's pieces: piece k at k * rec, piece 0 at rec0.  Chunks of the grid:
+  // part[t][chunk][head].  Balanced: slots 2 CTA and 2 CTA + 1 of G records each; the second is
+  // for the piece that starts its list (piece 0), whose CTA may end another one before.
+  const bool bal = it.b >= 0;
+  const size_t rec = (size_t)(bal ? 2 * G : p.n_heads) * (D + 2);
+  const size_t rec0 = bal ? (size_t)G * (D + 2) : 0;
+  auto record = [&](int h, int t, int head) {
+    return p.part + (bal ? ((size_t)it.slot * G + h) * (D + 2)
+                         : (size_t)t * p.n_split * rec + (size_t)head * (D + 2));
+  };
   for (int h = warp; h < np; h += C::NW) {         // a warp a pair
     const int row = h / G, t = t0 + row, head = head0 + h - row * G;
     const float inv = s_l[h] > 0.f ? 1.f / s_l[h] : 0.f;
-    float* dst = split ? p.part + ((size_t)t * p.n_split + c) * rec + (size_t)head * (D + 2)
+    float* dst = split ? record(h, t, head) + (it.piece ? it.piece * rec : rec0)
                        : p.out + ((size_t)t * p.n_heads + head) * D;
     float e[C::NW];
 #pragma unroll
@@ -581,36 +604,37 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D, PN>::NW, Q4Cfg<D, PN>::MIN_CTAS)
   }
   if (!split) return;
 
-  // ---- the group's last CTA (a ticket; nobody waits) merges its chunks by log-sum-exp: a warp
-  //      finds a pair's weights, then the threads fold the chunks' records, 16 loads in flight
+  // ---- the last CTA of the pieces (a ticket; nobody waits) merges them by log-sum-exp: a warp
+  //      finds a pair's weights, then the threads fold the pieces' records, 16 loads in flight
   __shared__ int s_last;
-  __threadfence();
   __syncthreads();
-  if (threadIdx.x == 0)
-    s_last = atomicInc(p.counters + (size_t)blockIdx.z * gridDim.y + blockIdx.y,
-                       (unsigned)(nchunks - 1)) == (unsigned)(nchunks - 1);
+  if (threadIdx.x == 0) {
+    __threadfence();  // the CTA's records (ordered before by the barrier), then the ticket
+    s_last = atomicInc(p.counters + (size_t)it.z * qp.columns + it.y, (unsigned)(pieces - 1)) ==
+             (unsigned)(pieces - 1);
+  }
   __syncthreads();
   if (!s_last) return;
   __threadfence();
-  float* wt = reinterpret_cast<float*>(smem);  // [pair][nchunks]
+  float* wt = reinterpret_cast<float*>(smem);  // [pair][pieces]
   for (int h = warp; h < np; h += C::NW) {
     const int row = h / G;
-    const float* src =
-        p.part + (size_t)(t0 + row) * p.n_split * rec + (size_t)(head0 + h - row * G) * (D + 2);
+    const float* src = record(h, t0 + row, head0 + h - row * G);
     float M = -INFINITY, Ls = 0.f;
-    for (int cc = lane; cc < nchunks; cc += 32) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(src + (size_t)cc * rec + D));
+    for (int cc = lane; cc < pieces; cc += 32) {
+      const float2 ml =
+          __ldcg(reinterpret_cast<const float2*>(src + (cc ? cc * rec : rec0) + D));
       const float mn = fmaxf(M, ml.x);
       if (mn != -INFINITY) Ls = Ls * __expf(M - mn) + ml.y * __expf(ml.x - mn);
       M = mn;
-      wt[h * nchunks + cc] = ml.x;
+      wt[h * pieces + cc] = ml.x;
     }
     const float Mw = warp_max(M);
     Ls = warp_sum(M == -INFINITY ? 0.f : Ls * __expf(M - Mw));
     const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
-    for (int cc = lane; cc < nchunks; cc += 32) {
-      const float m = wt[h * nchunks + cc];
-      wt[h * nchunks + cc] = m == -INFINITY ? 0.f : __expf(m - Mw) * inv;
+    for (int cc = lane; cc < pieces; cc += 32) {
+      const float m = wt[h * pieces + cc];
+      wt[h * pieces + cc] = m == -INFINITY ? 0.f : __expf(m - Mw) * inv;
     }
   }
   __syncthreads();
@@ -619,23 +643,112 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D, PN>::NW, Q4Cfg<D, PN>::MIN_CTAS)
   const int d = 2 * (threadIdx.x % TPP);
   for (int h = threadIdx.x / TPP; h < np; h += 32 * C::NW / TPP) {
     const int row = h / G, t = t0 + row, head = head0 + h - row * G;
-    const float* src = p.part + (size_t)t * p.n_split * rec + (size_t)head * (D + 2) + d;
-    const float* e = wt + h * nchunks;
+    const float* src = record(h, t, head) + d;
+    const float* e = wt + h * pieces;
     float2 a = make_float2(0.f, 0.f);
-    for (int cc = 0; cc < nchunks; cc += 16) {
+    for (int cc = 0; cc < pieces; cc += 16) {
       float2 v[16];
 #pragma unroll
-      for (int k = 0; k < 16; ++k)  // past the last chunk: the last one again, weight 0
-        v[k] = __ldcg(reinterpret_cast<const float2*>(src + (size_t)min(cc + k, nchunks - 1) * rec));
+      for (int k = 0; k < 16; ++k) {  // past the last piece: the last one again, weight 0
+        const int q = min(cc + k, pieces - 1);
+        v[k] = __ldcg(reinterpret_cast<const float2*>(src + (q ? q * rec : rec0)));
+      }
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
-        const float w = cc + k < nchunks ? e[cc + k] : 0.f;
+        const float w = cc + k < pieces ? e[cc + k] : 0.f;
         a.x = fmaf(v[k].x, w, a.x);
         a.y = fmaf(v[k].y, w, a.y);
       }
     }
     *reinterpret_cast<float2*>(p.out + ((size_t)t * p.n_heads + head) * D + d) =
         make_float2(gated(p, t, head, d, a.x), gated(p, t, head, d + 1, a.y));
+  }
+}
+
+template <int D, int PN>
+__global__ void __launch_bounds__(32 * Q4Cfg<D, PN>::NW, Q4Cfg<D, PN>::MIN_CTAS)
+    q4_mma_kernel(const Q4Params qp) {
+  using C = Q4Cfg<D, PN>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int s_pre[kQ4BalancedRows + 1];
+  const PartialParams& p = qp.base;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) {
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF) + warp * C::NST;
+    for (int st = 0; st < C::NST; ++st) mbar_init(&full[st], 1);
+    mbar_init_fence();
+  }
+  __syncwarp();  // the barriers, before any lane waits on one
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  uint32_t phases = 0;  // the parity each stage's next wait is for
+  // Balanced: one wave of CTAs, each with an equal share of all rows' tiles end to end (row by row,
+  // column by column).  s_pre: the rows' tiles added up.  What the loop goes by stays in shared
+  // memory: one copy of q4_item, with no more alive around it than the chunks of a grid need.
+  __shared__ long long s_f, s_end, s_per;
+  const int n_tok = p.n_tok, U = qp.columns, b = blockIdx.x;
+  if (qp.balanced) {
+    for (int r = threadIdx.x; r < n_tok; r += blockDim.x) {
+      int seq;
+      const Visible v(visible_row(p, r, b == 0, seq), p.window, p.n_sink);
+      const int base = (v.w0 & ~15) <= v.ns ? 0 : v.w0 & ~15, ns = base ? v.ns : 0;
+      s_pre[r + 1] = (ns + C::TP - 1) / C::TP + (v.L - base + C::TP - 1) / C::TP;
+    }
+    if (threadIdx.x == 0) s_pre[0] = 0;
+    __syncthreads();
+    if (warp == 0) {
+      constexpr int RPL = kQ4BalancedRows / 32;
+      int sum = 0;
+      for (int k = 0; k < RPL; ++k) sum += lane * RPL + k < n_tok ? s_pre[lane * RPL + k + 1] : 0;
+      int before = sum;
+#pragma unroll
+      for (int x = 1; x < 32; x *= 2) {
+        const int y = __shfl_up_sync(0xffffffffu, before, x);
+        if (lane >= x) before += y;
+      }
+      before -= sum;
+      for (int k = 0; k < RPL && lane * RPL + k < n_tok; ++k)
+        s_pre[lane * RPL + k + 1] = before += s_pre[lane * RPL + k + 1];
+    }
+    __syncthreads();
+    for (int r = b; r < n_tok; r += gridDim.x)  // rows that see nothing: zeros
+      if (s_pre[r + 1] == s_pre[r])
+        for (int i = threadIdx.x; i < p.n_heads * D; i += blockDim.x)
+          p.out[(size_t)r * p.n_heads * D + i] = 0.f;
+    if (threadIdx.x == 0) {
+      const long long total = (long long)U * s_pre[n_tok];
+      s_per = max((total + gridDim.x - 1) / gridDim.x, (long long)kQ4MinTiles);
+      s_f = b * s_per;
+      s_end = min(s_f + s_per, total);
+    }
+    __syncthreads();
+  }
+  for (;;) {
+    Q4Item it{(int)blockIdx.z, (int)blockIdx.y, 0, -1, (int)blockIdx.x, 0, 0};
+    if (qp.balanced) {
+      const long long f = s_f, per = s_per;
+      if (f >= s_end) return;
+      int z = 0;  // the last row that starts at or before f
+      for (int step = kQ4BalancedRows / 2; step; step /= 2)
+        if (z + step < n_tok && (long long)U * s_pre[z + step] <= f) z += step;
+      const int n = s_pre[z + 1] - s_pre[z];
+      const int off = static_cast<int>(f - (long long)U * s_pre[z]);
+      it.z = z;
+      it.y = off / n;
+      it.a = off - it.y * n;
+      it.b = static_cast<int>(min((long long)n, it.a + (s_end - f)));
+      const long long start = f - it.a;  // of the row's column
+      const int c0 = static_cast<int>(start / per);
+      it.pieces = static_cast<int>((start + n - 1) / per) - c0 + 1;
+      it.piece = b - c0;
+      it.slot = 2 * c0;
+      __syncthreads();
+      if (threadIdx.x == 0) s_f = f + (it.b - it.a);
+    }
+    q4_item<D, PN>(qp, smem, it, phases);
+    if (!qp.balanced) return;
+    fence_async_smem();  // the next copies follow this item's accesses
+    __syncthreads();
   }
 }
 

@@ -36,12 +36,19 @@ struct VisibleTiles {
 // n_sink what a row sees, base.chunk counts tiles, base.counters hold a word per (group, grid.y).
 struct Q4Params {
   PartialParams base;
-  int rows;  // rows of a group: their (row, head) pairs are at most 8
+  int rows;      // rows of a group: their (row, head) pairs are at most 8
+  int columns;   // KV heads x head split
+  int balanced;  // one wave of CTAs with equal shares (rows 1, n_tok <= kQ4BalancedRows)
   float k_scale, v_scale;
 };
 
 // positions of a tile of the 4-bit kernel: a warp's copies of 9 KB (D = 64: 4.6)
 __host__ __device__ constexpr int q4_tile(int head_dim) { return head_dim == 256 ? 32 : 64; }
+// CTAs of the 4-bit kernel on an SM, by their registers and rings; pn blocks of four pairs
+__host__ __device__ constexpr int q4_ctas_per_sm(int head_dim, int pn) {
+  return head_dim == 256 || (head_dim == 128 && pn > 1) ? 2 : 3;
+}
+constexpr int kQ4BalancedRows = 256, kQ4MinTiles = 8;
 constexpr int kQ4MaxSplit = 1024;  // chunks of a row at most
 constexpr int kWinRowsTile = 128;  // ... of the kernel for rows that share a sequence
 

@@ -16,9 +16,10 @@ bool q4_scale_ok(float s);  // append_q4.cu
 
 // Chunks of whole tiles, as many as fill the CTA slots of the GPU once at the rows' longest, within
 // these bounds.
-constexpr int kQ4CtasPerSm = 3;
-constexpr int kQ4MaxChunk = 2048, kQ4MinChunk = 256;
 constexpr int kWinCtasPerSm = 2;
+constexpr int kQ4MaxChunk = 2048, kQ4MinChunk = 256;
+// The balanced split cuts most lists at least once; it pays where a CTA's share is long.
+constexpr int kQ4BalancedTiles = 32;
 constexpr int kWinMaxChunk = 4096, kWinMinStages = 2;
 constexpr int kWinRowsMinPairs = 32;
 
@@ -72,7 +73,8 @@ gqa_status plan_visible(int n_tok, int n_seq, int n_heads, int n_kv_heads, int h
   const int rows = q4 && n_seq < n_tok ? 8 / (group / hs) : 1;
   const long long groups = (n_tok + rows - 1) / rows;
   const long long units = std::max(1LL, groups * n_kv_heads * hs);
-  const long long slots = (long long)(q4 ? kQ4CtasPerSm : kWinCtasPerSm) * num_sms;
+  const long long slots = (long long)(q4 ? q4_ctas_per_sm(head_dim, rows * (group / hs) > 4 ? 2 : 1) : kWinCtasPerSm) *
+                          num_sms;
   long long chunk = (units * tiles + slots - 1) / slots;
   chunk = std::max<long long>(chunk, q4 ? kQ4MinChunk / tile : kWinMinStages);
   chunk = std::min<long long>(chunk, (q4 ? kQ4MaxChunk : kWinMaxChunk) / tile);
@@ -90,6 +92,20 @@ gqa_status plan_visible(int n_tok, int n_seq, int n_heads, int n_kv_heads, int h
   const long long n_split = std::max(1LL, (tiles + chunk - 1) / chunk);
   if (n_split > (1 << 30) || (long long)n_kv_heads * hs > 65535)
     return fail(GQA_EUNSUPPORTED, "too many chunks or heads for one launch");
+  const char* fc = std::getenv("GQA_FORCE_CTAS");  // tests: a balanced grid of this many
+  const int forced_ctas = fc ? std::atoi(fc) : 0;
+  if (q4 && rows == 1 && n_tok <= kQ4BalancedRows && forced <= 0 &&
+      (forced_ctas > 0 ||
+       (units * n_split > slots && units * tiles >= kQ4BalancedTiles * slots))) {
+    const long long ctas = forced_ctas > 0 ? std::min(forced_ctas, 65535) : slots;
+    plan->n_split = plan->grid_x = (int)ctas;
+    plan->grid_y = plan->grid_z = 1;
+    plan->tile = tile;
+    plan->merge = plan->streamk = 1;
+    const size_t cnt = ((size_t)n_tok * n_kv_heads * hs * sizeof(uint32_t) + 255) / 256 * 256;
+    plan->ws_bytes = cnt + 2 * (size_t)ctas * (group / hs) * (head_dim + 2) * sizeof(float);
+    return GQA_OK;
+  }
   plan->chunk = (int)std::min<long long>(chunk * tile, INT_MAX / tile * tile);
   plan->n_split = (int)n_split;
   plan->tile = tile;
@@ -172,13 +188,16 @@ static gqa_status visible_common(int kind, const float* q, const void* kc, const
   p.n_split = plan.n_split;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.merge = plan.merge;
-  p.head_split = std::max(1, plan.grid_y / n_kv_heads);
+  p.head_split = 1;
+  if (q4)
+    while (p.group % p.head_split || p.group / p.head_split > 8) ++p.head_split;
   if (plan.merge && !q4 && plan.row_group > 1) {  // ws = [partials][n_valid]
     const size_t part = (size_t)n_tok * plan.n_split * n_heads * (head_dim + 2) * sizeof(float);
     p.part = static_cast<float*>(ws);
     p.n_valid = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + (part + 255) / 256 * 256);
   } else if (plan.merge) {  // ws = [arrival counters][partials]
-    const size_t cnt = ((size_t)n_tok * plan.grid_y * sizeof(uint32_t) + 255) / 256 * 256;
+    const size_t cnt =
+        ((size_t)n_tok * n_kv_heads * p.head_split * sizeof(uint32_t) + 255) / 256 * 256;
     p.counters = static_cast<unsigned int*>(ws);
     p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + cnt);
   }
@@ -191,6 +210,8 @@ static gqa_status visible_common(int kind, const float* q, const void* kc, const
   cudaError_t e;
   if (q4) {
     qp.rows = plan.row_group;
+    qp.columns = n_kv_heads * p.head_split;
+    qp.balanced = plan.streamk;
     qp.k_scale = k_scale;
     qp.v_scale = v_scale;
     e = launch_q4(head_dim, qp, grid, stream);

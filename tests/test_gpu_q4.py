@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import oracle
-from gpu_util import assert_close, dev, forced_chunk
+from gpu_util import assert_close, dev, forced_chunk, forced_ctas
 from q4_util import TOL, hidden, q4_cache, rows
 
 pytestmark = pytest.mark.gpu
@@ -170,6 +170,28 @@ def test_decode_window(D, window, n_sink, chunk):
         got = run_q4(q, cache, LENS, window=window, n_sink=n_sink).cpu().numpy()
     ref = oracle.decode_q4(q, *cache, LENS, D ** -0.5, window=window, n_sink=n_sink)
     assert_close(got, ref, TOL, f"window {window} sinks {n_sink} D {D}")
+
+
+@pytest.mark.parametrize("ctas", [1, 3, 7, 40, 500])
+@pytest.mark.parametrize("H,Hk,D", [(4, 1, 128), (16, 2, 128), (3, 3, 64), (12, 1, 256)])
+def test_decode_balanced(H, Hk, D, ctas):
+    """One wave of CTAs with equal shares of all lists: shares that hold several lists, lists over
+    many shares, empty rows, a workspace used twice."""
+    rng = np.random.default_rng(D + ctas)
+    lens = [0, 1, 2100, 63, 64, 65, 0, 700, 512, 513, 1030, 0]
+    cache = q4_cache(rng, lens, Hk, 2112, D)
+    q = rows(rng, len(lens), H, D)
+    gate = rows(rng, len(lens) * H * D)
+    with forced_ctas(ctas):
+        assert _gd().plan(len(lens), H, Hk, D, 2112, kind=_gd().KIND_Q4).streamk == 1
+        ws = _gd().alloc_workspace(len(lens), H, Hk, D, 2112, kind=_gd().KIND_Q4)
+        for window, n_sink in ((None, 0), (600, 70), (None, 0)):
+            got = run_q4(q, cache, lens, window=window, n_sink=n_sink, ws=ws).cpu().numpy()
+            ref = oracle.decode_q4(q, *cache, lens, D ** -0.5, window=window, n_sink=n_sink)
+            assert_close(got, ref, TOL, f"{ctas} CTAs, window {window}")
+            got = run_q4(q, cache, lens, window=window, n_sink=n_sink, ws=ws,
+                         gate=dev(gate)).cpu().numpy()
+            assert_close(got, oracle.output_gate(ref, gate.reshape(ref.shape)), TOL, "gate")
 
 
 @pytest.mark.parametrize("H,Hk,D", [(8, 2, 128), (4, 4, 64), (32, 2, 64), (12, 2, 256), (7, 1, 128)])
