@@ -29,6 +29,8 @@
 //        position are one run of D/16 bytes, at D = 128 under one scale.  Two positions' codes are
 //        interleaved nibble by nibble before the conversion.
 // Rows of 32 or 64 bytes are read without bank conflicts in k.q and two at a time at most in v.p.
+#include <atomic>
+
 #include "dispatch.h"
 #include "q4_common.cuh"
 #include "umma.cuh"
@@ -61,6 +63,9 @@ struct Q4Cfg {
   static constexpr int NST0 = QSMEM ? NST : NST - 1;  // tiles asked for before q is in
   static constexpr int BAR_OFF = RING + (QSMEM ? QF_BYTES : 0);
   static constexpr int SMEM = BAR_OFF + NW * NST * 8;
+  // a cluster's merge: this CTA's records, beside the merge area
+  static constexpr int CP_OFF = align_up(MERGE, 16);
+  static_assert(CP_OFF + NP * (D + 2) * 4 <= RING, "cluster records inside the rings");
   static_assert(QSMEM || QF_BYTES <= STAGE, "q's fragments fit a stage");
   static_assert(MIN_CTAS * (SMEM + 2304 + 1024) <= 228 * 1024, "MIN_CTAS fit an SM");
   static_assert(MERGE <= RING && NP * kQ4MaxSplit * 4 <= RING, "merge areas inside the rings");
@@ -216,6 +221,10 @@ __device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const
       if (it.piece == 0)  // nothing to see: zeros
         for (int i = threadIdx.x; i < np * D; i += blockDim.x)
           p.out[((size_t)(t0 + i / (G * D)) * p.n_heads + head0) * D + i % (G * D)] = 0.f;
+      if (p.cluster > 1) {  // the cluster's two barriers count every thread of every CTA
+        cluster_sync();
+        cluster_sync();
+      }
       return;
     }
   }
@@ -569,7 +578,7 @@ __device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const
     s_l[h] = Ls;
   }
   __syncthreads();
-  const bool split = pieces > 1;
+  const bool split = pieces > 1 || p.cluster > 1;
   // Records [D + 2] of a pair's pieces: piece k at k * rec, piece 0 at rec0.  Chunks of the grid:
   // part[t][chunk][head].  Balanced: slots 2 CTA and 2 CTA + 1 of G records each; the second is
   // for the piece that starts its list (piece 0), whose CTA may end another one before.
@@ -583,8 +592,9 @@ __device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const
   for (int h = warp; h < np; h += C::NW) {         // a warp a pair
     const int row = h / G, t = t0 + row, head = head0 + h - row * G;
     const float inv = s_l[h] > 0.f ? 1.f / s_l[h] : 0.f;
-    float* dst = split ? record(h, t, head) + (it.piece ? it.piece * rec : rec0)
-                       : p.out + ((size_t)t * p.n_heads + head) * D;
+    float* dst = p.cluster > 1 ? reinterpret_cast<float*>(smem + C::CP_OFF) + h * (D + 2)
+                 : split       ? record(h, t, head) + (it.piece ? it.piece * rec : rec0)
+                               : p.out + ((size_t)t * p.n_heads + head) * D;
     float e[C::NW];
 #pragma unroll
     for (int w = 0; w < C::NW; ++w) e[w] = s_w[w][h] * (split ? 1.f : inv);
@@ -603,6 +613,46 @@ __device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const
     if (split && lane == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(s_m[h], s_l[h]);
   }
   if (!split) return;
+  if (p.cluster > 1) {  // the chunks' CTAs are one cluster: each folds a part of the outputs from all
+                        // of their shared memories
+    cluster_sync();     // the records are in place
+    const uint32_t cp = smem_addr(smem + C::CP_OFF);
+    for (int idx = it.piece * 32 * C::NW + threadIdx.x; idx < np * (D / 2);
+         idx += pieces * 32 * C::NW) {
+      const int h = idx / (D / 2), d = 2 * (idx % (D / 2));
+      const uint32_t a = cp + static_cast<uint32_t>(h * (D + 2)) * 4u;
+      float m[kQ4MaxCluster], l[kQ4MaxCluster], M = -INFINITY;
+      float2 v[kQ4MaxCluster];
+#pragma unroll
+      for (int r = 0; r < kQ4MaxCluster; ++r) {
+        m[r] = -INFINITY;
+        l[r] = v[r].x = v[r].y = 0.f;
+        if (r < pieces) {
+          const uint32_t src = cluster_map(a, r);
+          m[r] = ld_cluster_f32(src + D * 4);
+          l[r] = ld_cluster_f32(src + (D + 1) * 4);
+          v[r].x = ld_cluster_f32(src + d * 4);
+          v[r].y = ld_cluster_f32(src + d * 4 + 4);
+        }
+        M = fmaxf(M, m[r]);
+      }
+      float2 y = make_float2(0.f, 0.f);
+      float Ls = 0.f;
+#pragma unroll
+      for (int r = 0; r < kQ4MaxCluster; ++r) {
+        const float e = m[r] == -INFINITY ? 0.f : __expf(m[r] - M);
+        y.x = fmaf(v[r].x, e, y.x);
+        y.y = fmaf(v[r].y, e, y.y);
+        Ls = fmaf(l[r], e, Ls);
+      }
+      const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
+      const int row = h / G, t = t0 + row, head = head0 + h - row * G;
+      *reinterpret_cast<float2*>(p.out + ((size_t)t * p.n_heads + head) * D + d) =
+          make_float2(gated(p, t, head, d, y.x * inv), gated(p, t, head, d + 1, y.y * inv));
+    }
+    cluster_sync();  // no CTA leaves while another reads its shared memory
+    return;
+  }
 
   // ---- the last CTA of the pieces (a ticket; nobody waits) merges them by log-sum-exp: a warp
   //      finds a pair's weights, then the threads fold the pieces' records, 16 loads in flight
@@ -752,8 +802,32 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D, PN>::NW, Q4Cfg<D, PN>::MIN_CTAS)
   }
 }
 
+// Clusters of n CTAs of this kernel that the GPU holds at once (asked once per size); 0 where the
+// size is not to be had.  More than 8 CTAs a cluster need the function's consent.
 template <int D, int PN>
-static cudaError_t launch_q4_d(const Q4Params& qp, dim3 grid, cudaStream_t s) {
+static int clusters_at_once(cudaLaunchConfig_t cfg, unsigned n) {
+  static std::atomic<int> known[kQ4MaxCluster + 1];  // 1 + the number
+  if (n < 2 || n > static_cast<unsigned>(kQ4MaxCluster)) return 0;
+  if (known[n].load() == 0) {
+    const void* fn = reinterpret_cast<const void*>(&q4_mma_kernel<D, PN>);
+    cudaLaunchAttribute at[1];
+    cluster_attrs(at, static_cast<int>(n), 0);
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(n);
+    int k = 0;
+    const bool ok =
+        (n <= 8 || cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+                       cudaSuccess) &&
+        cudaOccupancyMaxActiveClusters(&k, fn, &cfg) == cudaSuccess;
+    if (!ok) (void)cudaGetLastError();
+    known[n].store(1 + (ok ? k : 0));
+  }
+  return known[n].load() - 1;
+}
+
+template <int D, int PN>
+static cudaError_t launch_q4_d(Q4Params qp, dim3 grid, cudaStream_t s) {
   using C = Q4Cfg<D, PN>;
   const void* fn = reinterpret_cast<const void*>(&q4_mma_kernel<D, PN>);
   cudaError_t e = ensure_smem(fn, C::SMEM);
@@ -763,9 +837,13 @@ static cudaError_t launch_q4_d(const Q4Params& qp, dim3 grid, cudaStream_t s) {
   cfg.blockDim = dim3(32 * C::NW);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = s;
+  // a row's chunks merge inside a cluster where one wave of clusters holds the grid
+  const bool clus = !qp.balanced && grid.x > 1 &&
+                    clusters_at_once<D, PN>(cfg, grid.x) >= static_cast<long long>(grid.y) * grid.z;
+  qp.base.cluster = clus ? static_cast<int>(grid.x) : 0;
   cudaLaunchAttribute at[2];
   cfg.attrs = at;
-  cfg.numAttrs = cluster_attrs(at, 0, 1);
+  cfg.numAttrs = cluster_attrs(at, qp.base.cluster, 1);
   return cudaLaunchKernelEx(&cfg, &q4_mma_kernel<D, PN>, qp);
 }
 

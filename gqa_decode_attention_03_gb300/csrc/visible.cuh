@@ -50,6 +50,7 @@ __host__ __device__ constexpr int q4_ctas_per_sm(int head_dim, int pn) {
 }
 constexpr int kQ4BalancedRows = 256, kQ4MinTiles = 8;
 constexpr int kQ4MaxSplit = 1024;  // chunks of a row at most
+constexpr int kQ4MaxCluster = 16;  // ... that merge in a cluster
 constexpr int kWinRowsTile = 128;  // ... of the kernel for rows that share a sequence
 
 // Row t's length and sequence; values out of range are flagged (by the thread that `flag` names)
