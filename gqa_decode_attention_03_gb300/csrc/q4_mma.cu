@@ -30,6 +30,7 @@
 //        interleaved nibble by nibble before the conversion.
 // Rows of 32 or 64 bytes are read without bank conflicts in k.q and two at a time at most in v.p.
 #include <atomic>
+#include <type_traits>
 
 #include "dispatch.h"
 #include "q4_common.cuh"
@@ -39,16 +40,16 @@
 
 namespace gqa {
 
-template <int D, int PN_>
+template <int D, int PN_, int NW_>
 struct Q4Cfg {
   static constexpr int PN = PN_, NP = 4 * PN;       // column blocks, pairs
-  static constexpr int NW = 4;                      // warps
+  static constexpr int NW = NW_;                    // warps
   static constexpr int RB = D / 2, SB = D / 16;     // bytes of a position's codes and scales
   static constexpr int TP = q4_tile(D);             // positions of a tile, worked on SP at a time
   static constexpr int SP = 32, NB = SP / 16;       // 16-position blocks
   static constexpr int STAGE = 2 * TP * (RB + SB);  // [K codes][V codes][K scales][V scales]
   static constexpr int NST = D == 64 ? 4 : 2;
-  static constexpr int MIN_CTAS = q4_ctas_per_sm(D, PN);
+  static constexpr int MIN_CTAS = NW == 4 ? q4_ctas_per_sm(D, PN) : 1;
   static constexpr int KS = D / 16;                 // k-steps of k.q
   static constexpr int KW = D / 32;                 // words of a thread's codes of a K position
   static constexpr int VW = D / 64;                 // ... of a V position
@@ -127,10 +128,10 @@ struct Q4Item {
   int slot;             // balanced: record slot of piece 0's CTA
 };
 
-template <int D, int PN>
+template <int D, int PN, int NW>
 __device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const Q4Item& it,
                                         uint32_t& phases) {
-  using C = Q4Cfg<D, PN>;
+  using C = Q4Cfg<D, PN, NW>;
   const PartialParams& p = qp.base;
   __shared__ Q4Run s_runs[C::NW][9];
   __shared__ float s_amax[C::NW][C::NP];
@@ -142,20 +143,22 @@ __device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
 
-  // this warp's quarter of q, asked for before anything else is known: pair 4 pn + gid / 2
-  constexpr int QW = C::KS / C::NW;
+  // this warp's k-steps of q, asked for before anything else is known: pair 4 pn + gid / 2
+  constexpr int QW = cmax(C::KS / C::NW, 1);  // k-steps a warp (D = 64: half of eight warps none)
+  const bool qon = warp * QW < C::KS;
   float4 qx[PN][QW];
 #pragma unroll
   for (int pn = 0; pn < PN; ++pn) {
     const int pair = 4 * pn + (gid >> 1), row = pair < np ? pair / G : 0;
+    const bool on = pair < np && qon;
     const float* qrow =
         p.q + ((size_t)(t0 + row) * p.n_heads + head0 + (pair < np ? pair - row * G : 0)) * D;
 #pragma unroll
     for (int e = 0; e < QW; ++e) {
       const int ks = warp * QW + e, w = ks / 2;  // word of the thread's run of codes, half of it
       const int d = (w / 4) * 128 + (D == 64 ? 16 : 32) * tig + 8 * (w % 4) + 4 * (ks & 1);
-      qx[pn][e] = pair < np ? __ldg(reinterpret_cast<const float4*>(qrow + d))
-                            : make_float4(0.f, 0.f, 0.f, 0.f);
+      qx[pn][e] = on ? __ldg(reinterpret_cast<const float4*>(qrow + d))
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
 
@@ -257,7 +260,7 @@ __device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const
 
   // ---- q's B fragments: the pair's row scaled by a power of two to [1, 2) as f16 hi or lo; sm
   //      takes the power, the softmax scale and the cache's scale of K back in.  Each warp makes
-  //      those of its quarter of the k-steps: pair 4 pn + gid / 2, part gid & 1.
+  //      those of its k-steps: pair 4 pn + gid / 2, part gid & 1.
   uint2* qf = reinterpret_cast<uint2*>(smem + C::QF_OFF) + lane;
   float sm[PN];
   {
@@ -288,7 +291,7 @@ __device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const
         uint2 hv, lv;
         split_hi_lo(qx[pn][e].x * f, qx[pn][e].y * f, hv.x, lv.x);
         split_hi_lo(qx[pn][e].z * f, qx[pn][e].w * f, hv.y, lv.y);
-        qf[(pn * C::KS + warp * QW + e) * 32] = gid & 1 ? lv : hv;
+        if (qon) qf[(pn * C::KS + warp * QW + e) * 32] = gid & 1 ? lv : hv;
       }
     }
   }
@@ -715,10 +718,10 @@ __device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const
   }
 }
 
-template <int D, int PN>
-__global__ void __launch_bounds__(32 * Q4Cfg<D, PN>::NW, Q4Cfg<D, PN>::MIN_CTAS)
+template <int D, int PN, int NW>
+__global__ void __launch_bounds__(32 * Q4Cfg<D, PN, NW>::NW, Q4Cfg<D, PN, NW>::MIN_CTAS)
     q4_mma_kernel(const Q4Params qp) {
-  using C = Q4Cfg<D, PN>;
+  using C = Q4Cfg<D, PN, NW>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_pre[kQ4BalancedRows + 1];
   const PartialParams& p = qp.base;
@@ -795,7 +798,7 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D, PN>::NW, Q4Cfg<D, PN>::MIN_CTAS)
       __syncthreads();
       if (threadIdx.x == 0) s_f = f + (it.b - it.a);
     }
-    q4_item<D, PN>(qp, smem, it, phases);
+    q4_item<D, PN, NW>(qp, smem, it, phases);
     if (!qp.balanced) return;
     fence_async_smem();  // the next copies follow this item's accesses
     __syncthreads();
@@ -804,12 +807,12 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D, PN>::NW, Q4Cfg<D, PN>::MIN_CTAS)
 
 // Clusters of n CTAs of this kernel that the GPU holds at once (asked once per size); 0 where the
 // size is not to be had.  More than 8 CTAs a cluster need the function's consent.
-template <int D, int PN>
+template <int D, int PN, int NW>
 static int clusters_at_once(cudaLaunchConfig_t cfg, unsigned n) {
   static std::atomic<int> known[kQ4MaxCluster + 1];  // 1 + the number
   if (n < 2 || n > static_cast<unsigned>(kQ4MaxCluster)) return 0;
   if (known[n].load() == 0) {
-    const void* fn = reinterpret_cast<const void*>(&q4_mma_kernel<D, PN>);
+    const void* fn = reinterpret_cast<const void*>(&q4_mma_kernel<D, PN, NW>);
     cudaLaunchAttribute at[1];
     cluster_attrs(at, static_cast<int>(n), 0);
     cfg.attrs = at;
@@ -826,10 +829,10 @@ static int clusters_at_once(cudaLaunchConfig_t cfg, unsigned n) {
   return known[n].load() - 1;
 }
 
-template <int D, int PN>
+template <int D, int PN, int NW>
 static cudaError_t launch_q4_d(Q4Params qp, dim3 grid, cudaStream_t s) {
-  using C = Q4Cfg<D, PN>;
-  const void* fn = reinterpret_cast<const void*>(&q4_mma_kernel<D, PN>);
+  using C = Q4Cfg<D, PN, NW>;
+  const void* fn = reinterpret_cast<const void*>(&q4_mma_kernel<D, PN, NW>);
   cudaError_t e = ensure_smem(fn, C::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -839,22 +842,27 @@ static cudaError_t launch_q4_d(Q4Params qp, dim3 grid, cudaStream_t s) {
   cfg.stream = s;
   // a row's chunks merge inside a cluster where one wave of clusters holds the grid
   const bool clus = !qp.balanced && grid.x > 1 &&
-                    clusters_at_once<D, PN>(cfg, grid.x) >= static_cast<long long>(grid.y) * grid.z;
+                    clusters_at_once<D, PN, NW>(cfg, grid.x) >= static_cast<long long>(grid.y) * grid.z;
   qp.base.cluster = clus ? static_cast<int>(grid.x) : 0;
   cudaLaunchAttribute at[2];
   cfg.attrs = at;
   cfg.numAttrs = cluster_attrs(at, qp.base.cluster, 1);
-  return cudaLaunchKernelEx(&cfg, &q4_mma_kernel<D, PN>, qp);
+  return cudaLaunchKernelEx(&cfg, &q4_mma_kernel<D, PN, NW>, qp);
 }
 
 cudaError_t launch_q4(int head_dim, const Q4Params& qp, dim3 grid, cudaStream_t s) {
-  // a CTA's pairs, at most 8, in one block of four columns or two
+  // a CTA's pairs, at most 8, in one block of four columns or two; a grid that leaves no SM a second
+  // CTA has eight warps a CTA
   const int np = qp.rows * (qp.base.group / qp.base.head_split);
-  if (head_dim == 64)
-    return np <= 4 ? launch_q4_d<64, 1>(qp, grid, s) : launch_q4_d<64, 2>(qp, grid, s);
-  if (head_dim == 128)
-    return np <= 4 ? launch_q4_d<128, 1>(qp, grid, s) : launch_q4_d<128, 2>(qp, grid, s);
-  return np <= 4 ? launch_q4_d<256, 1>(qp, grid, s) : launch_q4_d<256, 2>(qp, grid, s);
+  auto go = [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    if (qp.wide)
+      return np <= 4 ? launch_q4_d<D, 1, 8>(qp, grid, s) : launch_q4_d<D, 2, 8>(qp, grid, s);
+    return np <= 4 ? launch_q4_d<D, 1, 4>(qp, grid, s) : launch_q4_d<D, 2, 4>(qp, grid, s);
+  };
+  if (head_dim == 64) return go(std::integral_constant<int, 64>());
+  if (head_dim == 128) return go(std::integral_constant<int, 128>());
+  return go(std::integral_constant<int, 256>());
 }
 
 }  // namespace gqa

@@ -38,6 +38,7 @@ struct Q4Params {
   PartialParams base;
   int rows;      // rows of a group: their (row, head) pairs are at most 8
   int columns;   // KV heads x head split
+  int wide;      // eight warps a CTA, one CTA an SM
   int balanced;  // one wave of CTAs with equal shares (rows 1, n_tok <= kQ4BalancedRows)
   float k_scale, v_scale;
 };

@@ -14,12 +14,18 @@ namespace gqa {
 
 bool q4_scale_ok(float s);  // append_q4.cu
 
-// Chunks of whole tiles, as many as fill the CTA slots of the GPU once at the rows' longest, within
-// these bounds.
+// 4-bit caches (plan_visible), GB300, one box, us:
+// - A grid that would give every CTA slot kQ4LongShare tiles or more is cut into chunks of kQ4Chunk
+//   positions (64 rows of up to 4096: 52.5 with 1024, 51.7 with 2048), or, where lists are kQ4LongList
+//   positions or longer, into equal shares of all lists in one wave (16 ragged rows of up to 32768: 69.8
+//   chunked, 63.4; 64 rows of up to 8192: 95.4 against 87.0, of up to 4096:
+//   71.9 against 51.7, a list's start and end weighing more).
+// - A smaller one that has an SM for every list runs one CTA of eight warps an SM, a list in as many
+//   chunks as there are SMs (one row of 48 heads over 4, 8191 positions: 16.7 against 18.2 with four
+//   warps; 32 rows of two sequences, window 2048: 13.5 against 17.7).
+constexpr int kQ4Chunk = 2048, kQ4LongShare = 32, kQ4LongList = 10240;
+// Windowed f16 rows: as many chunks as fill the CTA slots once, of at most kWinMaxChunk positions.
 constexpr int kWinCtasPerSm = 2;
-constexpr int kQ4MaxChunk = 2048, kQ4MinChunk = 256;
-// The balanced split cuts most lists at least once; it pays where a CTA's share is long.
-constexpr int kQ4BalancedTiles = 32;
 constexpr int kWinMaxChunk = 4096, kWinMinStages = 2;
 constexpr int kWinRowsMinPairs = 32;
 
@@ -73,15 +79,23 @@ gqa_status plan_visible(int n_tok, int n_seq, int n_heads, int n_kv_heads, int h
   const int rows = q4 && n_seq < n_tok ? 8 / (group / hs) : 1;
   const long long groups = (n_tok + rows - 1) / rows;
   const long long units = std::max(1LL, groups * n_kv_heads * hs);
-  const long long slots = (long long)(q4 ? q4_ctas_per_sm(head_dim, rows * (group / hs) > 4 ? 2 : 1) : kWinCtasPerSm) *
-                          num_sms;
-  long long chunk = (units * tiles + slots - 1) / slots;
-  chunk = std::max<long long>(chunk, q4 ? kQ4MinChunk / tile : kWinMinStages);
-  chunk = std::min<long long>(chunk, (q4 ? kQ4MaxChunk : kWinMaxChunk) / tile);
+  const long long slots =
+      (long long)num_sms *
+      (q4 ? q4_ctas_per_sm(head_dim, rows * (group / hs) > 4 ? 2 : 1) : kWinCtasPerSm);
+  const bool big = units * tiles >= kQ4LongShare * slots;  // (q4)
+  long long chunk = kQ4Chunk / tile;
+  if (!q4)
+    chunk = std::min<long long>(std::max<long long>((units * tiles + slots - 1) / slots, kWinMinStages),
+                                kWinMaxChunk / tile);
   const char* f = std::getenv("GQA_FORCE_CHUNK");
   const int forced = f ? std::atoi(f) : 0;
   if (forced > 0) {
     chunk = (forced + tile - 1) / tile;
+  } else if (q4 && !big && units <= num_sms) {
+    // one CTA of eight warps an SM, a tile a warp at the least, at most 16 chunks a row (a cluster)
+    const long long most = std::min<long long>(std::min<long long>(num_sms / units, kQ4MaxCluster),
+                                               std::max(1LL, tiles / 8));
+    chunk = (tiles + most - 1) / most;
   } else if (!q4 && chunk < tiles) {
     // a split grid that fits the GPU merges each row in a cluster of up to 8 chunk CTAs
     const long long c8 = (tiles + 7) / 8;
@@ -95,8 +109,7 @@ gqa_status plan_visible(int n_tok, int n_seq, int n_heads, int n_kv_heads, int h
   const char* fc = std::getenv("GQA_FORCE_CTAS");  // tests: a balanced grid of this many
   const int forced_ctas = fc ? std::atoi(fc) : 0;
   if (q4 && rows == 1 && n_tok <= kQ4BalancedRows && forced <= 0 &&
-      (forced_ctas > 0 ||
-       (units * n_split > slots && units * tiles >= kQ4BalancedTiles * slots))) {
+      (forced_ctas > 0 || (big && n >= kQ4LongList))) {
     const long long ctas = forced_ctas > 0 ? std::min(forced_ctas, 65535) : slots;
     plan->n_split = plan->grid_x = (int)ctas;
     plan->grid_y = plan->grid_z = 1;
@@ -212,6 +225,9 @@ static gqa_status visible_common(int kind, const float* q, const void* kc, const
     qp.rows = plan.row_group;
     qp.columns = n_kv_heads * p.head_split;
     qp.balanced = plan.streamk;
+    st = GQA_OK;
+    qp.wide = !plan.streamk && (long long)plan.grid_x * plan.grid_y * plan.grid_z <=
+                                   current_sm_count(&st);
     qp.k_scale = k_scale;
     qp.v_scale = v_scale;
     e = launch_q4(head_dim, qp, grid, stream);
