@@ -8,7 +8,7 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
-#include "common.cuh"
+#include "partial_mma.cuh"
 
 namespace gqa {
 
@@ -28,6 +28,16 @@ __device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t (&h)[4]) {
       "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
       : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
       : "r"(w));
+}
+
+// e4m3 bytes in bits 0-7 and 16-23 of x -> an f16x2 of their values.
+__device__ __forceinline__ __half2 e4m3x2_to_f16x2(uint32_t x) {
+  const uint32_t h = (x & 0x007f007fu) << 7;  // the values times 2^-8
+  return __hmul2(*reinterpret_cast<const __half2*>(&h), __float2half2_rn(256.f));
+}
+
+__device__ __forceinline__ uint32_t mul_h2(uint32_t a, __half2 s) {
+  return h2_bits(__hmul2(*reinterpret_cast<const __half2*>(&a), s));
 }
 
 // The sequence holding row r of a ragged batch: the last s with row_off[s] <= r, or -1.  All 32

@@ -73,16 +73,6 @@ struct Q4Cfg {
   static constexpr float RESCALE_LOG2 = 8.f;
 };
 
-// e4m3 bytes in bits 0-7 and 16-23 of x -> an f16x2 of their values.
-__device__ __forceinline__ __half2 e4m3x2_to_f16x2(uint32_t x) {
-  const uint32_t h = (x & 0x007f007fu) << 7;  // the values times 2^-8
-  return __hmul2(*reinterpret_cast<const __half2*>(&h), __float2half2_rn(256.f));
-}
-
-__device__ __forceinline__ uint32_t mul_h2(uint32_t a, __half2 s) {
-  return h2_bits(__hmul2(*reinterpret_cast<const __half2*>(&a), s));
-}
-
 // A run of a group's rows that share a sequence: the union of what they see, as tiles.
 struct Q4Run {
   int seq, tiles0;  // sequence; index of its first tile in the group's list

@@ -27,14 +27,24 @@ constexpr int kQ4Chunk = 2048, kQ4LongShare = 32, kQ4LongList = 10240;
 // Windowed f16 rows: as many chunks as fill the CTA slots once, of at most kWinMaxChunk positions.
 constexpr int kWinCtasPerSm = 2;
 constexpr int kWinMaxChunk = 4096, kWinMinStages = 2;
-constexpr int kWinRowsMinPairs = 32;
+// Rows sharing a sequence: pairs of a sequence and (4-bit) products of rows, heads and positions from
+// which the kernel for 128 pairs a CTA is the faster one.  f16, window 2048, G = 4, rows of one
+// sequence: 16 rows 15.6 us against 20.1 row by row, 512 rows 34 against 273; 8 rows of each of 8
+// sequences 40.0 against 41.3.  4-bit, 8000 positions: 8 rows 24.3 against 18.5 with 8 pairs a CTA,
+// 16 rows 25.6 against 29.6, 512 rows 98 against 731; 16 rows of 2 sequences, window 2048, 22.2
+// against 13.6.
+constexpr int kRowsMinPairs = 32;
+constexpr long long kQ4RowsMinWork = 3LL << 20;
 
-// Rows that share a sequence go to the kernel that serves 128 (row, head) pairs a CTA when there
-// are enough of them.
-static bool window_rows_grouped(int n_tok, int n_seq, int group, int head_dim) {
-  const char* r = std::getenv("GQA_F16_ROWS");  // "off": one CTA per row (tests, comparison)
-  if (r && std::strcmp(r, "off") == 0) return false;
-  return head_dim != 256 && (long long)n_tok * group >= (long long)kWinRowsMinPairs * n_seq;
+// Whether rows that may share a sequence go to the kernel that serves 128 (row, head) pairs a CTA;
+// n: positions a row sees at most.
+static bool rows_grouped(bool q4, int n_tok, int n_seq, int n_heads, int group, int head_dim,
+                         long long n) {
+  const char* r = std::getenv(q4 ? "GQA_Q4_ROWS" : "GQA_F16_ROWS");
+  if (head_dim == 256 || n_seq >= n_tok || (r && std::strcmp(r, "off") == 0)) return false;
+  if (r && std::strcmp(r, "on") == 0) return true;  // tests, comparison
+  return (long long)n_tok * group >= (long long)kRowsMinPairs * n_seq &&
+         (!q4 || (long long)n_tok * n_heads * n >= kQ4RowsMinWork);
 }
 
 gqa_status plan_visible(int n_tok, int n_seq, int n_heads, int n_kv_heads, int head_dim,
@@ -49,7 +59,7 @@ gqa_status plan_visible(int n_tok, int n_seq, int n_heads, int n_kv_heads, int h
   }
   const bool q4 = kind == GQA_KIND_Q4;
   const int group = n_heads / n_kv_heads;
-  if (!q4 && window_rows_grouped(n_tok, n_seq, group, head_dim)) {
+  if (rows_grouped(q4, n_tok, n_seq, n_heads, group, head_dim, n)) {
     const int r = 128 / group;
     const long long groups = (n_tok + r - 1) / r;
     const long long most = std::max(1LL, (n + kWinRowsTile - 1) / kWinRowsTile);
@@ -204,7 +214,9 @@ static gqa_status visible_common(int kind, const float* q, const void* kc, const
   p.head_split = 1;
   if (q4)
     while (p.group % p.head_split || p.group / p.head_split > 8) ++p.head_split;
-  if (plan.merge && !q4 && plan.row_group > 1) {  // ws = [partials][n_valid]
+  const bool grouped = rows_grouped(q4, n_tok, n_seq, n_heads, p.group, head_dim,
+                                    budget > 0 ? std::min(max_len, budget) : max_len);
+  if (plan.merge && grouped) {  // ws = [partials][n_valid]
     const size_t part = (size_t)n_tok * plan.n_split * n_heads * (head_dim + 2) * sizeof(float);
     p.part = static_cast<float*>(ws);
     p.n_valid = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + (part + 255) / 256 * 256);
@@ -221,29 +233,30 @@ static gqa_status visible_common(int kind, const float* q, const void* kc, const
   p.pdl = 1;
   const dim3 grid(plan.grid_x, plan.grid_y, plan.grid_z);
   cudaError_t e;
-  if (q4) {
+  st = GQA_OK;
+  const int sms = current_sm_count(&st);
+  const long long ctas = (long long)plan.grid_x * plan.grid_y * plan.grid_z;
+  qp.k_scale = k_scale;
+  qp.v_scale = v_scale;
+  if (q4 && grouped) {
+    e = launch_q4_rows(head_dim, qp, grid, stream);
+  } else if (q4) {
     qp.rows = plan.row_group;
     qp.columns = n_kv_heads * p.head_split;
     qp.balanced = plan.streamk;
-    st = GQA_OK;
-    qp.wide = !plan.streamk && (long long)plan.grid_x * plan.grid_y * plan.grid_z <=
-                                   current_sm_count(&st);
-    qp.k_scale = k_scale;
-    qp.v_scale = v_scale;
+    qp.wide = !plan.streamk && ctas <= sms;
     e = launch_q4(head_dim, qp, grid, stream);
   } else {
     CUtensorMap tk, tv;
     st = encode_f16_cache(kc, vc, n_seq, cache_cap, n_kv_heads, head_dim, plan.tile, &tk, &tv);
     if (st != GQA_OK) return st;
-    st = GQA_OK;
-    p.cluster = plan.merge && (long long)plan.grid_x * plan.grid_y * plan.grid_z <=
-                                  current_sm_count(&st);
-    e = plan.row_group > 1 ? launch_window_rows(head_dim, tk, tv, p, grid, stream)
-                           : launch_f16_window(head_dim, tk, tv, p, grid, stream);
-    if (e == cudaSuccess && plan.row_group > 1 && plan.merge)
-      e = launch_merge(head_dim, p.part, p.n_valid, plan.n_split, n_tok, n_heads, out, stream,
-                       p.gate, p.gate_stride, /*after_partials=*/true);
+    p.cluster = plan.merge && ctas <= sms;
+    e = grouped ? launch_window_rows(head_dim, tk, tv, qp, grid, stream)
+                : launch_f16_window(head_dim, tk, tv, p, grid, stream);
   }
+  if (e == cudaSuccess && grouped && plan.merge)
+    e = launch_merge(head_dim, p.part, p.n_valid, plan.n_split, n_tok, n_heads, out, stream, p.gate,
+                     p.gate_stride, /*after_partials=*/true);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return cuda_fail(e, q4 ? "attn_decode_q4 launch" : "attn_decode_f16_window launch");

@@ -1,5 +1,5 @@
-// window_rows_umma.cu -- windowed f16 attention of rows that share a sequence (a chunk of a prompt)
-// on the fifth-generation tensor cores.
+// window_rows_umma.cu -- attention of rows that share a sequence (a chunk of a prompt) on the
+// fifth-generation tensor cores, over f16 caches through a window and over 4-bit caches.
 //
 // One CTA serves the 128 / G consecutive query rows of a group for one KV head: their (row, head)
 // pairs are the M = 128 rows of its MMAs, two softmax threads each, so every K/V tile is read once
@@ -10,7 +10,10 @@
 //                    the running maximum moves only when a tile exceeds it by 2^8; written back
 //                    over S in TMEM as f16 hi and lo parts (64 columns each)
 //   O += P . V       fp32 in TMEM, A = P from TMEM, two MMAs a k-step
-// hi + lo keep ~22 bits of q and of the weights; K and V are f16 as they are.
+// hi + lo keep ~22 bits of q and of the weights; K and V are f16 as they are, or 4-bit values, exact
+// in f16 (q4_common.cuh).  f16 tiles arrive by TMA; 4-bit ones through four warps, a thread a
+// position, that keep the next tile's codes in registers while they write this one's values into the
+// same swizzled layout: 128 pairs share the conversion of a tile that q4_mma.cu makes for 8.
 //
 // Three S/P buffers: the issuer's order S(j+1), PV(j) gives the softmax of tile j the time of
 // PV(j-1) and S(j+1), and no MMA waits for the one just before it.  The tiles of a group are those
@@ -22,13 +25,14 @@
 // values, and a group that meets one is computed again at the end without matrix products
 // (rows_plain), which skips hidden positions.
 #include "dispatch.h"
+#include "q4_common.cuh"
 #include "umma.cuh"
 #include "visible.cuh"
 #include "visible_dispatch.h"
 
 namespace gqa {
 
-template <int D>
+template <int D, bool Q4>
 struct WinRowsCfg {
   static constexpr int M = 128, TP = kWinRowsTile;
   static constexpr int NBOX = D / 64;
@@ -39,7 +43,9 @@ struct WinRowsCfg {
   static constexpr int NB = 3;                     // S/P buffers in TMEM
   static constexpr int O_COL = NB * TP, TMEM_COLS = 512;
   static constexpr int KS_S = D / 16;
-  static constexpr int NSW = 8, PRODUCER = 8, ISSUER = 9, PV_ISSUER = 10, THREADS = 352;
+  static constexpr int NSW = 8, PRODUCER = 8, NLW = Q4 ? 4 : 1;  // softmax, loading warps
+  static constexpr int ISSUER = PRODUCER + NLW, PV_ISSUER = ISSUER + 1, THREADS = 32 * (PV_ISSUER + 1);
+  static constexpr int LOADS = Q4 ? 32 * NLW : 1;  // arrivals that make a tile full
   static constexpr int Q_OFF = (NK + NV) * KT;
   static constexpr int NBAR = 2 * NK + 2 * NV + 3 * NB + 2;
   static constexpr int BAR_OFF = Q_OFF + 2 * Q_PART;
@@ -65,6 +71,7 @@ struct WinRowsTable {
   int nruns, dirty;
   float mx[2][2][128];  // [tile parity][half][row]: maxima of the halves; at the end their sums
   float m[128], l[128];  // the pairs' final state
+  float sm[128];         // 4-bit: factor of a pair's scores (q is scaled to [1, 2) by a power of two)
 };
 
 struct WinTile {
@@ -173,13 +180,13 @@ struct WinOut {
   bool nan;       // the sum is NaN: see keep_nan
   float* dst;
   __device__ __forceinline__ WinOut(const PartialParams& p_, int t_, int head_, int c_, float m_,
-                                    float l_)
+                                    float l_, float v_scale)
       : p(p_), t(t_), head(head_), c(c_), m(m_), l(l_), nan(l_ != l_) {
     if (nan) {
       m = kNanMax;
       l = INFINITY;
     }
-    f = p.merge ? 1.f : 1.f / l;
+    f = p.merge ? v_scale : v_scale / l;
     dst = p.merge ? p.part + (((size_t)t * p.n_split + c) * p.n_heads + head) * (D + 2)
                   : p.out + ((size_t)t * p.n_heads + head) * D;
   }
@@ -203,7 +210,7 @@ __device__ void rows_plain(const PartialParams& p, const WinRowsTable& tb, int t
   const int G = p.group;
   const __half* kc = static_cast<const __half*>(p.kc);
   const __half* vc = static_cast<const __half*>(p.vc);
-  for (int pair = warp; pair < nr * G; pair += WinRowsCfg<D>::NSW) {
+  for (int pair = warp; pair < nr * G; pair += WinRowsCfg<D, false>::NSW) {
     const int row = pair / G, t = t0 + row, head = g * G + pair % G;
     const Visible v(tb.len[row], p.window, p.n_sink);
     float q[DPL], o[DPL], m = -INFINITY, l = 0.f;
@@ -232,12 +239,55 @@ __device__ void rows_plain(const PartialParams& p, const WinRowsTable& tb, int t
         for (int e = 0; e < DPL; ++e) o[e] = fmaf(wgt, __half2float(vc[at + e]), o[e] * corr);
       }
     }
-    const WinOut<D> out(p, t, head, c, m, l);
+    const WinOut<D> out(p, t, head, c, m, l, 1.f);
 #pragma unroll
     for (int e = 0; e < DPL; ++e) out.dst[lane * DPL + e] = out.value(lane * DPL + e, o[e]);
     if (lane == 0) out.stats();
   }
 }
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
+// A position's codes and scales of one side, and their values as a row of a swizzled f16 tile.
+template <int D>
+struct Q4Row {
+  uint4 codes[D / 32];
+  uint32_t scales[D / 64];
+  __device__ __forceinline__ void load(const void* kc, const void* sc, size_t row, bool on) {
+    const uint4* c = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kc) + row * (D / 2));
+    const uint32_t* s =
+        reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(sc) + row * (D / 16));
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) codes[k] = on ? __ldg(c + k) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k) scales[k] = on ? __ldg(s + k) : 0u;
+  }
+  __device__ __forceinline__ void store(uint8_t* tile, int r) const {
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) {
+      const uint32_t w[4] = {codes[k].x, codes[k].y, codes[k].z, codes[k].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {  // 8 dims: 16-byte piece 4 k + e of the row, scale 2 k + e / 2
+        const int ch = 4 * k + e, sc = 2 * k + e / 2;
+        const uint32_t b = (scales[sc / 4] >> (8 * (sc % 4))) & 0x7fu;
+        const __half2 s2 = e4m3x2_to_f16x2(b | b << 16);
+        uint32_t h[4];
+        e2m1x8_to_f16x2(w[e], h);
+        *reinterpret_cast<uint4*>(tile + (ch >> 3) * (kWinRowsTile * 128) + r * 128 +
+                                  (((ch & 7) ^ (r & 7)) << 4)) =
+            make_uint4(mul_h2(h[0], s2), mul_h2(h[1], s2), mul_h2(h[2], s2), mul_h2(h[3], s2));
+      }
+    }
+  }
+};
 
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {  // one instruction for two sums
   float2 r;
@@ -257,11 +307,12 @@ __device__ __forceinline__ void tmem_ld_landed(uint32_t (&r)[N]) {
   for (int e = 0; e < N; ++e) asm volatile("" : "+r"(r[e]));
 }
 
-template <int D>
-__global__ void __launch_bounds__(WinRowsCfg<D>::THREADS, 1)
+template <int D, bool Q4>
+__global__ void __launch_bounds__(WinRowsCfg<D, Q4>::THREADS, 1)
     window_rows_kernel(const __grid_constant__ CUtensorMap tmK,
-                       const __grid_constant__ CUtensorMap tmV, const PartialParams p) {
-  using C = WinRowsCfg<D>;
+                       const __grid_constant__ CUtensorMap tmV, const Q4Params qp) {
+  using C = WinRowsCfg<D, Q4>;
+  const PartialParams& p = qp.base;
   extern __shared__ uint8_t smem_raw[];
   __shared__ WinRowsTable tb;
   const int c = blockIdx.x, g = blockIdx.y;
@@ -304,9 +355,20 @@ __global__ void __launch_bounds__(WinRowsCfg<D>::THREADS, 1)
     for (int u = 0; u < NQ; ++u) {
       const unsigned f = threadIdx.x + u * 32 * C::NSW, qr = f / (D / 4), c4 = f % (D / 4);
       const unsigned ch = c4 >> 1;
+      float qs = p.scale_log2;
+      if constexpr (Q4) {  // the pair's row to [1, 2); its scores are multiplied back
+        float m = fmaxf(fmaxf(fabsf(x[u].x), fabsf(x[u].y)), fmaxf(fabsf(x[u].z), fabsf(x[u].w)));
+#pragma unroll
+        for (int o = 1; o < D / 4; o *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const uint32_t e = min(max(__float_as_uint(m) >> 23, 1u), 253u);
+        const float sm = p.scale_log2 * qp.k_scale * __uint_as_float(e << 23);
+        qs = copysignf(__uint_as_float((254u - e) << 23), sm);  // 2^(127 - e)
+        // (a scale of 0: not 0, so that -infinity stays one)
+        if (c4 == 0) tb.sm[qr] = fmaxf(fabsf(sm), 1.2e-38f);
+      }
       uint2 hv, lv;
-      split_hi_lo(x[u].x * p.scale_log2, x[u].y * p.scale_log2, hv.x, lv.x);
-      split_hi_lo(x[u].z * p.scale_log2, x[u].w * p.scale_log2, hv.y, lv.y);
+      split_hi_lo(x[u].x * qs, x[u].y * qs, hv.x, lv.x);
+      split_hi_lo(x[u].z * qs, x[u].w * qs, hv.y, lv.y);
       uint8_t* dst = sQ + (ch >> 3) * C::Q_BOX + qr * 128 + (((ch & 7) ^ (qr & 7)) << 4) +
                      (c4 & 1) * 8;
       *reinterpret_cast<uint2*>(dst) = hv;
@@ -322,11 +384,11 @@ __global__ void __launch_bounds__(WinRowsCfg<D>::THREADS, 1)
     if (lane == 0) {
       tb.dirty = 0;
       for (int i = 0; i < C::NK; ++i) {
-        mbar_init(&k_full[i], 1);
+        mbar_init(&k_full[i], C::LOADS);
         mbar_init(&k_empty[i], 1);
       }
       for (int i = 0; i < C::NV; ++i) {
-        mbar_init(&v_full[i], 1);
+        mbar_init(&v_full[i], C::LOADS);
         mbar_init(&v_empty[i], 1);
       }
       for (int i = 0; i < C::NB; ++i) {
@@ -337,8 +399,10 @@ __global__ void __launch_bounds__(WinRowsCfg<D>::THREADS, 1)
       mbar_init(&drain[0], 1);
       mbar_init(&drain[1], 1);
       mbar_init_fence();
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
+      if constexpr (!Q4) {
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+      }
     }
     __syncwarp();
     win_build(tb, nr, p.window, p.n_sink, lane);
@@ -360,6 +424,45 @@ __global__ void __launch_bounds__(WinRowsCfg<D>::THREADS, 1)
     if (c == 0 && !p.merge)  // no row sees anything: zeros (a merge writes them otherwise)
       for (int i = threadIdx.x; i < nr * G * D; i += C::THREADS)
         p.out[((size_t)(t0 + i / (G * D)) * p.n_heads + g * G) * D + i % (G * D)] = 0.f;
+  } else if (Q4 && warp >= C::PRODUCER && warp < C::ISSUER) {
+    // ---- 4-bit tiles: thread r holds position r's codes and writes their values
+    if constexpr (Q4) {
+      const int r = threadIdx.x - 32 * C::PRODUCER;
+      const uint8_t* ksc = reinterpret_cast<const uint8_t*>(p.ksc);
+      const uint8_t* vsc = reinterpret_cast<const uint8_t*>(p.vsc);
+      Q4Row<D> kr, vr;
+      int k = 0;
+      size_t row = 0;
+      bool on = false;
+      auto place = [&](int j) {  // of tile j's position r
+        const WinTile w = win_tile(tb, i0 + j, k);
+        on = w.start + r < w.end;
+        row = ((size_t)w.seq * p.n_kv_heads + g) * p.cache_cap + w.start + r;
+      };
+      place(0);
+      kr.load(p.kc, ksc, row, on);
+      vr.load(p.vc, vsc, row, on);
+      bool ok = true;
+      for (int j = 0; j < nt; ++j) {
+        const int sk = j % C::NK, sv = j % C::NV;
+        ok = __all_sync(0xffffffffu,
+                        j < C::NK || mbar_wait(&k_empty[sk], ((j / C::NK) - 1) & 1));
+        if (!ok) break;
+        kr.store(sK + sk * C::KT, r);
+        if (j + 1 < nt) place(j + 1);
+        if (j + 1 < nt) kr.load(p.kc, ksc, row, on);
+        fence_async_smem();
+        mbar_arrive(&k_full[sk]);
+        ok = __all_sync(0xffffffffu,
+                        j < C::NV || mbar_wait(&v_empty[sv], ((j / C::NV) - 1) & 1));
+        if (!ok) break;
+        vr.store(sV + sv * C::KT, r);
+        if (j + 1 < nt) vr.load(p.vc, vsc, row, on);
+        fence_async_smem();
+        mbar_arrive(&v_full[sv]);
+      }
+      if (!ok && lane == 0) flag_error(p.err, GQA_ERR_TIMEOUT);
+    }
   } else if (warp == C::PRODUCER) {  // ---- TMA: K(j), then V(j - 1)
     if (lane == 0) {
       bool ok = true;
@@ -461,6 +564,7 @@ __global__ void __launch_bounds__(WinRowsCfg<D>::THREADS, 1)
     const Visible vis(rv ? tb.len[row] : 0, p.window, p.n_sink);
     const int run = rv ? tb.run[row] : -1;
     const uint32_t t_row = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const float sm = Q4 ? tb.sm[i] : 1.f;  // q holds the whole factor for f16 caches
     // After a wait has run out none is tried again, but every warp walks all tiles, so that the
     // barriers of the epilogue are met; the call flags GQA_ERR_TIMEOUT.
     bool ok = true;
@@ -492,6 +596,7 @@ __global__ void __launch_bounds__(WinRowsCfg<D>::THREADS, 1)
 #pragma unroll
       for (int e = 0; e < 64; ++e) mq[e & 3] = fmaxf(mq[e & 3], __uint_as_float(s[e]));
       float mt = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+      if constexpr (Q4) mt *= sm;
       // the row's other half: its maximum, and the word that it has read its columns of S, over
       // which both halves write P
       tb.mx[j & 1][h][i] = mt;
@@ -523,8 +628,9 @@ __global__ void __launch_bounds__(WinRowsCfg<D>::THREADS, 1)
       uint32_t ph[32], pl[32];
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
-        float2 x = add2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])),
-                        make_float2(-mu, -mu));
+        float2 x = make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+        x = Q4 ? fma2(x, make_float2(sm, sm), make_float2(-mu, -mu))
+               : add2(x, make_float2(-mu, -mu));
         x.x = ex2_approx(x.x);
         x.y = ex2_approx(x.y);
         lq[e & 1] = add2(lq[e & 1], x);
@@ -539,30 +645,32 @@ __global__ void __launch_bounds__(WinRowsCfg<D>::THREADS, 1)
       lq[0] = add2(lq[0], lq[1]);
       l_run += lq[0].x + lq[0].y;
       tmem_st_wait();
-      // V rows behind the run's positions are zeroed; a tile that some row of the group does not
-      // see whole is searched for values that are not finite
-      const int nvis = min(C::TP, w.end - w.start);
-      const WinRun& r = tb.runs[k];
-      const bool all_see = tb.nruns == 1 && ((w.start >= r.w0_max && w.start + nvis <= r.end_min) ||
-                                             w.start + nvis <= r.ns_min);
-      if (nvis < C::TP || !all_see) {
-        const int st = j % C::NV;
-        wait(&v_full[st], (j / C::NV) & 1);
-        uint8_t* v = sV + st * C::KT;
-        bool bad = false;
-        for (int e = threadIdx.x; e < C::NBOX * C::TP * 8; e += 32 * C::NSW) {  // 16-byte pieces
-          uint4* x = reinterpret_cast<uint4*>(v + e * 16);
-          if ((e / 8) % C::TP >= nvis) {
-            *x = make_uint4(0u, 0u, 0u, 0u);
-          } else if (!all_see) {
-            const uint4 y = *x;  // a half is not finite if its magnitude is 0x7c00 or more
-            bad |= ((((y.x & 0x7fff7fffu) + 0x04000400u) | ((y.y & 0x7fff7fffu) + 0x04000400u) |
-                     ((y.z & 0x7fff7fffu) + 0x04000400u) | ((y.w & 0x7fff7fffu) + 0x04000400u)) &
-                    0x80008000u) != 0;
+      // f16: V rows behind the run's positions are zeroed; a tile that some row of the group does
+      // not see whole is searched for values that are not finite (4-bit values always are)
+      if constexpr (!Q4) {
+        const int nvis = min(C::TP, w.end - w.start);
+        const WinRun& r = tb.runs[k];
+        const bool all_see = tb.nruns == 1 && ((w.start >= r.w0_max && w.start + nvis <= r.end_min) ||
+                                               w.start + nvis <= r.ns_min);
+        if (nvis < C::TP || !all_see) {
+          const int st = j % C::NV;
+          wait(&v_full[st], (j / C::NV) & 1);
+          uint8_t* v = sV + st * C::KT;
+          bool bad = false;
+          for (int e = threadIdx.x; e < C::NBOX * C::TP * 8; e += 32 * C::NSW) {  // 16-byte pieces
+            uint4* x = reinterpret_cast<uint4*>(v + e * 16);
+            if ((e / 8) % C::TP >= nvis) {
+              *x = make_uint4(0u, 0u, 0u, 0u);
+            } else if (!all_see) {
+              const uint4 y = *x;  // a half is not finite if its magnitude is 0x7c00 or more
+              bad |= ((((y.x & 0x7fff7fffu) + 0x04000400u) | ((y.y & 0x7fff7fffu) + 0x04000400u) |
+                       ((y.z & 0x7fff7fffu) + 0x04000400u) | ((y.w & 0x7fff7fffu) + 0x04000400u)) &
+                      0x80008000u) != 0;
+            }
           }
+          if (bad) tb.dirty = 1;
+          fence_async_smem();
         }
-        if (bad) tb.dirty = 1;
-        fence_async_smem();
       }
       tc_fence_before();
       mbar_arrive(&p_full[b]);
@@ -594,7 +702,8 @@ __global__ void __launch_bounds__(WinRowsCfg<D>::THREADS, 1)
     }
     named_bar_sync(1, 32 * C::NSW);
     for (int pair = warp; pair < nr * G; pair += C::NSW) {
-      const WinOut<D> out(p, t0 + pair / G, g * G + pair % G, c, tb.m[pair], tb.l[pair]);
+      const WinOut<D> out(p, t0 + pair / G, g * G + pair % G, c, tb.m[pair], tb.l[pair],
+                          Q4 ? qp.v_scale : 1.f);
       const float2* src = reinterpret_cast<const float2*>(reinterpret_cast<float*>(sK) + pair * OS);
 #pragma unroll
       for (int q = 0; q < D / 64; ++q) {
@@ -606,7 +715,8 @@ __global__ void __launch_bounds__(WinRowsCfg<D>::THREADS, 1)
     }
     if (!ok && lane == 0) flag_error(p.err, GQA_ERR_TIMEOUT);
     named_bar_sync(1, 32 * C::NSW);
-    if (tb.dirty) rows_plain<D>(p, tb, t0, nr, g, c, i0, i1, warp, lane);
+    if constexpr (!Q4)
+      if (tb.dirty) rows_plain<D>(p, tb, t0, nr, g, c, i0, i1, warp, lane);
   }
   tc_fence_before();
   __syncthreads();
@@ -616,11 +726,11 @@ __global__ void __launch_bounds__(WinRowsCfg<D>::THREADS, 1)
   }
 }
 
-template <int D>
-static cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const PartialParams& p,
+template <int D, bool Q4>
+static cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const Q4Params& qp,
                             dim3 grid, cudaStream_t s) {
-  using C = WinRowsCfg<D>;
-  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(&window_rows_kernel<D>), C::SMEM);
+  using C = WinRowsCfg<D, Q4>;
+  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(&window_rows_kernel<D, Q4>), C::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
@@ -630,12 +740,19 @@ static cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const 
   cudaLaunchAttribute at[2];
   cfg.attrs = at;
   cfg.numAttrs = cluster_attrs(at, 0, 1);
-  return cudaLaunchKernelEx(&cfg, &window_rows_kernel<D>, tk, tv, p);
+  return cudaLaunchKernelEx(&cfg, &window_rows_kernel<D, Q4>, tk, tv, qp);
 }
 
 cudaError_t launch_window_rows(int head_dim, const CUtensorMap& tk, const CUtensorMap& tv,
-                               const PartialParams& p, dim3 grid, cudaStream_t s) {
-  return head_dim == 64 ? launch_d<64>(tk, tv, p, grid, s) : launch_d<128>(tk, tv, p, grid, s);
+                               const Q4Params& qp, dim3 grid, cudaStream_t s) {
+  return head_dim == 64 ? launch_d<64, false>(tk, tv, qp, grid, s)
+                        : launch_d<128, false>(tk, tv, qp, grid, s);
+}
+
+cudaError_t launch_q4_rows(int head_dim, const Q4Params& qp, dim3 grid, cudaStream_t s) {
+  const CUtensorMap none{};
+  return head_dim == 64 ? launch_d<64, true>(none, none, qp, grid, s)
+                        : launch_d<128, true>(none, none, qp, grid, s);
 }
 
 }  // namespace gqa

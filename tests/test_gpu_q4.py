@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import oracle
-from gpu_util import assert_close, dev, forced_chunk, forced_ctas
+from gpu_util import _env, assert_close, dev, forced_chunk, forced_ctas
 from q4_util import TOL, hidden, q4_cache, rows
 
 pytestmark = pytest.mark.gpu
@@ -203,10 +203,63 @@ def test_decode_rows_sharing_sequences(H, Hk, D, window):
     lens = list(range(401, 420)) + [5, 0, 1] + list(range(90, 98)) + [420, 300, 9, 64, 9]
     cache = q4_cache(rng, [16, 120, 430], Hk, 432, D)
     q = rows(rng, len(seq), H, D)
-    with forced_chunk(96 if window is None else None):
-        got = run_q4(q, cache, lens, seq, window=window, n_sink=3).cpu().numpy()
     ref = oracle.decode_q4(q, *cache, lens, D ** -0.5, seq_of=seq, window=window, n_sink=3)
-    assert_close(got, ref, TOL, "shared sequences")
+    # the kernel for 128 pairs a CTA (not at D = 256) and the one for up to 8, split and not
+    for rows_env, chunk in (("on", None), (None, None), ("off", 96)):
+        with _env(GQA_Q4_ROWS=rows_env), forced_chunk(chunk):
+            got = run_q4(q, cache, lens, seq, window=window, n_sink=3).cpu().numpy()
+        assert_close(got, ref, TOL, f"shared sequences, {rows_env}, {chunk}")
+
+
+@pytest.mark.parametrize("H,Hk,D", [(2, 2, 64), (8, 2, 128), (32, 2, 128), (12, 2, 64), (6, 2, 256)])
+def test_many_rows_of_several_sequences(H, Hk, D):
+    """300 rows in runs of 1 to 60 of five sequences, lengths from 0 on: several runs in a group, a
+    run over several groups; a grid split over positions and one that is not."""
+    rng = np.random.default_rng(D + H)
+    seq, lens = [], []
+    while len(seq) < 300:
+        s, m, n0 = int(rng.integers(5)), int(rng.integers(1, 61)), int(rng.integers(0, 900))
+        seq += [s] * m
+        lens += [min(960, n0 + i) for i in range(m)]
+    seq, lens = seq[:300], lens[:300]
+    last = [max([n for n, t in zip(lens, seq) if t == s] + [0]) for s in range(5)]
+    cache = q4_cache(rng, last, Hk, 960, D, 0.5, 4.0)
+    q = rows(rng, 300, H, D) * np.float32(3)
+    gate = rows(rng, 300 * H * D)
+    for window, n_sink, scale in ((None, 0, D ** -0.5), (150, 4, D ** -0.5), (33, 200, -0.1)):
+        for T in (300, 40):
+            with _env(GQA_Q4_ROWS="on"):
+                got = run_q4(q[:T], cache, lens[:T], seq[:T], window=window, n_sink=n_sink,
+                             scale=scale, k_scale=0.5, v_scale=4.0,
+                             gate=dev(gate[:T * H * D])).cpu().numpy()
+            ref = oracle.decode_q4(q[:T], *cache, lens[:T], scale, seq_of=seq[:T], window=window,
+                                   n_sink=n_sink, k_scale=0.5, v_scale=4.0)
+            ref = oracle.output_gate(ref, gate[:T * H * D].reshape(ref.shape))
+            # values of v_scale 4: four times the error; scores of 3 q: three times
+            assert_close(got / 4, ref / 4, 3 * TOL, f"window {window} rows {T}")
+
+
+def test_prompt_chunk_scales_and_zero_scale():
+    """A chunk of causal rows on the kernel for 128 pairs: queries and cache scales far from 1, a
+    softmax scale of 0 (the mean of what is seen), a NaN query."""
+    rng = np.random.default_rng(21)
+    T, H, Hk, D = 40, 8, 2, 128
+    lens = [100 + r for r in range(T)]
+    cache = q4_cache(rng, [140], Hk, 144, D, 2.0 ** -20, 2.0 ** 30)
+    q = rows(rng, T, H, D)
+    for qmul, scale in ((2.0 ** 30, 2.0 ** -10 * D ** -0.5), (2.0 ** -30, 2.0 ** 50 * D ** -0.5),
+                        (1.0, 0.0)):
+        kw = dict(scale=scale, k_scale=2.0 ** -20, v_scale=2.0 ** 30)
+        with _env(GQA_Q4_ROWS="on"):
+            got = run_q4(q * np.float32(qmul), cache, lens, [0] * T, **kw).cpu().numpy()
+        ref = oracle.decode_q4(q * np.float32(qmul), *cache, lens, seq_of=[0] * T, **kw)
+        assert_close(got / 2.0 ** 30, ref / 2.0 ** 30, TOL, f"q times {qmul}")
+    q[3, 2, 5] = np.nan
+    with _env(GQA_Q4_ROWS="on"):
+        got = run_q4(q, cache, lens, [0] * T, k_scale=2.0 ** -20, v_scale=2.0 ** 30).cpu().numpy()
+    assert np.isnan(got[3, 2]).all()
+    got[3, 2] = 0
+    assert np.isfinite(got).all()
 
 
 @pytest.mark.parametrize("k_scale,v_scale,scale,qmul", [
