@@ -15,10 +15,11 @@
 // position, that keep the next tile's codes in registers while they write this one's values into the
 // same swizzled layout: 128 pairs share the conversion of a tile that q4_mma.cu makes for 8.
 //
-// Three S/P buffers: the issuer's order S(j+1), PV(j) gives the softmax of tile j the time of
-// PV(j-1) and S(j+1), and no MMA waits for the one just before it.  The tiles of a group are those
-// of the union of its rows' visible positions, sequence by sequence where a group's rows belong to
-// several (consecutive rows of one sequence form a run; a row's weights are 0 outside its run).
+// S is issued by one thread and P . V by another, so that S(j + 1) and PV(j - 1) run while the softmax
+// of tile j does.  O adds up kWinDrain tiles, then joins a sum of its own in TMEM.  The tiles of a
+// group are those of the union of its rows' visible positions, sequence by sequence where a group's
+// rows belong to several (consecutive rows of one sequence form a run; a row's weights are 0 outside
+// its run).
 //
 // A hidden position weighs 0, but 0 times an infinity or NaN is NaN.  V rows that no row of the run
 // sees are zeroed in shared memory; in a tile that only some rows see whole, V is searched for such
@@ -32,6 +33,11 @@
 
 namespace gqa {
 
+// Tiles after which O joins its fp32 sum.  The tensor cores cut an accumulator's low bits at every
+// instruction, 16 a tile: without the sum 512 rows through a window of 2048 were 5.2e-6 off (2-norm),
+// joined every 4, 3, 2 tiles 1.4e-6, 1.2e-6, 1.0e-6, in 35.1 us, 35.6, 35.6, 36.6.
+constexpr int kWinDrain = 3;
+
 template <int D, bool Q4>
 struct WinRowsCfg {
   static constexpr int M = 128, TP = kWinRowsTile;
@@ -40,8 +46,9 @@ struct WinRowsCfg {
   static constexpr int KT = NBOX * BOX;            // a K or V tile
   static constexpr int NK = 2, NV = 2;             // ring slots
   static constexpr int Q_BOX = M * 128, Q_PART = NBOX * Q_BOX;
-  static constexpr int NB = 3;                     // S/P buffers in TMEM
-  static constexpr int O_COL = NB * TP, TMEM_COLS = 512;
+  static constexpr int NB = D == 128 ? 2 : 3;      // S/P buffers in TMEM
+  static constexpr int O_COL = NB * TP, A_COL = O_COL + D, TMEM_COLS = 512;  // O, and its sum
+  static constexpr int DRAIN = kWinDrain;          // tiles that O adds up before it joins the sum
   static constexpr int KS_S = D / 16;
   static constexpr int NSW = 8, PRODUCER = 8, NLW = Q4 ? 4 : 1;  // softmax, loading warps
   static constexpr int ISSUER = PRODUCER + NLW, PV_ISSUER = ISSUER + 1, THREADS = 32 * (PV_ISSUER + 1);
@@ -52,7 +59,7 @@ struct WinRowsCfg {
   static constexpr int TAB_OFF = align_up(BAR_OFF + NBAR * 8 + 16, 16);
   static constexpr int SMEM = 1024 + TAB_OFF;
   static constexpr float RESCALE_LOG2 = 8.f;
-  static_assert(O_COL + D <= TMEM_COLS, "TMEM columns");
+  static_assert(A_COL + D <= TMEM_COLS, "TMEM columns");
   static_assert(TP == 128 && M == 128, "one P column pair per S column");
 };
 
@@ -307,6 +314,25 @@ __device__ __forceinline__ void tmem_ld_landed(uint32_t (&r)[N]) {
   for (int e = 0; e < N; ++e) asm volatile("" : "+r"(r[e]));
 }
 
+// sum (+)= o over D / 2 columns of this thread's lane, rounded to nearest.
+template <int D>
+__device__ __forceinline__ void win_join(uint32_t o_col, uint32_t a_col, bool first) {
+#pragma unroll 1
+  for (int q = 0; q < D / 64; ++q) {
+    uint32_t o[32], a[32];
+    tmem_ld32(o_col + 32 * q, o);
+    tmem_ld32(a_col + 32 * q, a);
+    tmem_ld_landed(o);
+    tmem_ld_landed(a);
+    if (!first) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(a[e]));
+    }
+    tmem_st32(a_col + 32 * q, o);
+  }
+}
+
 template <int D, bool Q4>
 __global__ void __launch_bounds__(WinRowsCfg<D, Q4>::THREADS, 1)
     window_rows_kernel(const __grid_constant__ CUtensorMap tmK,
@@ -520,14 +546,14 @@ __global__ void __launch_bounds__(WinRowsCfg<D, Q4>::THREADS, 1)
           tc_fence_after();
           const uint32_t sk = smem_addr(sK + st * C::KT);
 #pragma unroll
-          for (int part = 0; part < 2; ++part)
+          for (int part = 1; part >= 0; --part)  // lo first: its roundings are of small sums
 #pragma unroll
             for (int kk = 0; kk < C::KS_S; ++kk)
               umma_f16(tbase + b * C::TP,
                        umma_desc_sw128(
                            q_addr + part * C::Q_PART + (kk >> 2) * C::Q_BOX + (kk & 3) * 32, 16, 1024),
                        umma_desc_sw128(sk + (kk >> 2) * C::BOX + (kk & 3) * 32, 16, 1024), id,
-                       part + kk > 0 ? 1u : 0u);
+                       part == 0 || kk > 0 ? 1u : 0u);
           umma_commit(&s_full[b]);
           umma_commit(&k_empty[st]);
         }
@@ -547,7 +573,7 @@ __global__ void __launch_bounds__(WinRowsCfg<D, Q4>::THREADS, 1)
             for (int part = 0; part < 2; ++part)
               umma_f16_ta(tbase + C::O_COL, pa + part * (C::TP / 2) + kk * 8,
                           umma_desc_sw128(sv + kk * 2048, C::BOX, 1024), kIdO,
-                          j + kk + part > 0 ? 1u : 0u);
+                          j % C::DRAIN + kk + part > 0 ? 1u : 0u);
           umma_commit(&pv_done[b]);
           umma_commit(&v_empty[st]);
         }
@@ -611,8 +637,9 @@ __global__ void __launch_bounds__(WinRowsCfg<D, Q4>::THREADS, 1)
         tc_fence_after();
         const float corr = resc ? ex2_approx(m_run - mt) : 1.f;
 #pragma unroll 1
-        for (int q = 0; q < D / 64; ++q) {  // this half's D / 2 columns
-          const uint32_t col = t_row + C::O_COL + h * (D / 2) + 32 * q;
+        for (int q = 0; q < D / 32; ++q) {  // this half's D / 2 columns of O and of its sum
+          if (q >= D / 64 && j <= C::DRAIN) break;  // nothing has joined the sum yet
+          const uint32_t col = t_row + (q < D / 64 ? C::O_COL : C::A_COL - D / 2) + h * (D / 2) + 32 * q;
           uint32_t o[32];
           tmem_ld32(col, o);
           tmem_ld_landed(o);
@@ -620,6 +647,7 @@ __global__ void __launch_bounds__(WinRowsCfg<D, Q4>::THREADS, 1)
           for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
           tmem_st32(col, o);
         }
+        tmem_st_wait();
         l_run *= corr;
       }
       if (grow) m_run = mt;
@@ -644,6 +672,11 @@ __global__ void __launch_bounds__(WinRowsCfg<D, Q4>::THREADS, 1)
       tmem_st32(t_row + b * C::TP + C::TP / 2 + 32 * h, pl);
       lq[0] = add2(lq[0], lq[1]);
       l_run += lq[0].x + lq[0].y;
+      if (j > 0 && j % C::DRAIN == 0) {  // O of the last DRAIN tiles joins the sum
+        wait(&pv_done[(j - 1) % C::NB], ((j - 1) / C::NB) & 1);
+        tc_fence_after();
+        win_join<D>(t_row + C::O_COL + h * (D / 2), t_row + C::A_COL + h * (D / 2), j == C::DRAIN);
+      }
       tmem_st_wait();
       // f16: V rows behind the run's positions are zeroed; a tile that some row of the group does
       // not see whole is searched for values that are not finite (4-bit values always are)
@@ -689,9 +722,16 @@ __global__ void __launch_bounds__(WinRowsCfg<D, Q4>::THREADS, 1)
     float* so = reinterpret_cast<float*>(sK) + i * OS + h * (D / 2);
 #pragma unroll
     for (int q = 0; q < D / 64; ++q) {
-      uint32_t o[32];
+      uint32_t o[32], a[32];
       tmem_ld32(t_row + C::O_COL + h * (D / 2) + 32 * q, o);
+      tmem_ld32(t_row + C::A_COL + h * (D / 2) + 32 * q, a);
       tmem_ld_landed(o);
+      tmem_ld_landed(a);
+      if (nt > C::DRAIN) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(a[e]));
+      }
 #pragma unroll
       for (int e = 0; e < 32; e += 4)
         *reinterpret_cast<uint4*>(so + 32 * q + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
