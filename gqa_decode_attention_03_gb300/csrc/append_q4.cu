@@ -1,14 +1,19 @@
 // append_q4.cu -- rows into and out of the 4-bit cache (kv_append_q4, kv_read_q4).
 //
-// A thread holds 8 consecutive dims of a (row, KV head) of K and of V: 32 bytes of fp32 and 4 bytes
-// of codes each, so a warp's loads and stores cover whole 128-byte lines; two threads share the
-// scale of 16 dims.  Threads are numbered dim slice first, then the row within a block of 16 rows,
-// then the KV head: a row block of one head is one run of the head-major cache, so that its scales
-// (8 bytes a position at D = 128) meet in whole 32-byte sectors.
+// A CTA takes 16 rows of one KV head, K and V: where they belong to one sequence, one run of the
+// head-major cache, so that its scales (8 bytes a position at D = 128) meet in whole 32-byte sectors.
+// A thread holds 8 consecutive dims of a row, 4 where it writes fp32, so that every load and store of
+// a warp covers whole 32-byte sectors; two threads share the scale of 16 dims in appending.  New rows
+// are asked for before their place is known: their address does not depend on it.
+//
+// Bound by memory: 21600 rows of 8 heads of 128 dims appended and read back as fp32 in 63.0 us on
+// GB300, 405 MB at 6.4 TB/s; six sequences of up to 8192 rows read in 38.8 us, 228 MB at 5.9 TB/s.
+// With the codes found by comparisons alone appending was bound by instructions (95 us in all).
 #include <cuda_runtime_api.h>
 
 #include <cmath>
 #include <cstdio>
+#include <type_traits>
 
 #include "gqa_decode.h"
 #include "q4_common.cuh"
@@ -18,7 +23,6 @@ namespace gqa {
 void set_last_error(const char* msg);  // host.cu: the text gqa_last_error() returns
 
 constexpr int kRowBlock = 16;
-constexpr int kQ4Threads = 128;
 
 struct Q4Rows {
   uint8_t *kq, *vq, *ksc, *vsc;
@@ -30,61 +34,81 @@ struct Q4Rows {
   float k_scale, v_scale;  // append: their inverses
 };
 
-// Where the thread's 8 dims are: the batch's element and the cache's (row, slice); false when the
-// thread has no row.  Every lane of the warp has to call it.
-template <int D>
-__device__ __forceinline__ bool q4_place(const Q4Rows& a, long long& elem, long long& crow,
-                                         int& slice) {
-  constexpr int TPR = D / 8;                       // threads per (row, head): 8, 16 or 32
-  constexpr int RPW = 32 / TPR;                    // rows of a warp
-  const long long i = (long long)blockIdx.x * kQ4Threads + threadIdx.x;
-  slice = static_cast<int>(i % TPR);
-  const long long u = i / TPR;                     // (row block, head, row)
-  const long long per = (long long)kRowBlock * a.hk;
-  const long long rb = u / per;
-  const int head = static_cast<int>(u % per / kRowBlock);
-  const long long r = rb * kRowBlock + u % kRowBlock;
-  const long long end = __ldg(a.row_off + a.n_seq);
-  const bool in = r < a.n_rows && r < end;
-  // a warp's rows are RPW consecutive ones of one head (kRowBlock is a multiple of RPW)
-  const int r_first = __shfl_sync(0xffffffffu, static_cast<int>(min(r, (long long)INT32_MAX)), 0);
+// Threads of a CTA with DPT dims of ROWS rows at a time.
+template <int D, int DPT, int ROWS>
+constexpr int kQ4Threads = ROWS * (D / DPT);
+
+// A row of the batch, the thread's first element there, its KV head.
+struct Q4Slot {
+  int r, head;
+  long long elem;
+};
+// The thread's row of rows j, j + 1, .. j + ROWS - 1 of the CTA's block.
+template <int D, int DPT>
+__device__ __forceinline__ Q4Slot q4_slot(const Q4Rows& a, int j) {
+  const unsigned rb = blockIdx.x / static_cast<unsigned>(a.hk);
+  Q4Slot s;
+  s.head = static_cast<int>(blockIdx.x - rb * a.hk);
+  const long long r = (long long)rb * kRowBlock + j + threadIdx.x / (D / DPT);
+  s.r = static_cast<int>(r < INT32_MAX ? r : INT32_MAX);
+  s.elem = (r * a.hk + s.head) * D + threadIdx.x % (D / DPT) * DPT;
+  return s;
+}
+
+// The cache row of the thread's row; false when no sequence holds it or its position is none of the
+// cache's (flagged).  Every lane of the warp has to call it; a warp's rows are consecutive.
+template <int D, int DPT>
+__device__ __forceinline__ bool q4_place(const Q4Rows& a, const Q4Slot& sl, long long& crow) {
+  constexpr int RPW = D / DPT >= 32 ? 1 : 32 / (D / DPT);  // rows of a warp
+  const int end = min(__ldg(a.row_off + a.n_seq), a.n_rows);
+  const int r_first = __shfl_sync(0xffffffffu, sl.r, 0);
   int s = -1;
 #pragma unroll
   for (int k = 0; k < RPW; ++k) {
-    if (r_first + k >= a.n_rows || r_first + k >= end) break;
+    if (r_first >= end - k) break;  // (r_first + k >= end, without overflow)
     const int f = ragged_find(a.row_off, a.n_seq, r_first + k);
-    if (r == r_first + k) s = f;
+    if (sl.r == r_first + k) s = f;
   }
-  if (!in) return false;
+  if (sl.r >= end) return false;
   const int first = s < 0 ? 0 : __ldg(a.row_off + s);
-  if (s < 0 || r < first || r >= __ldg(a.row_off + s + 1)) {
+  if (s < 0 || sl.r < first || sl.r >= __ldg(a.row_off + s + 1)) {
     flag_error(a.err, GQA_ERR_SEQ_RANGE);
     return false;
   }
-  const long long pos = (long long)__ldg(a.t0 + s) + (r - first);
+  const long long pos = (long long)__ldg(a.t0 + s) + (sl.r - first);
   if (pos < 0 || pos >= a.cap) {
     flag_error(a.err, GQA_ERR_KVLEN_RANGE);
     return false;
   }
-  elem = (r * a.hk + head) * D + slice * 8;
-  crow = ((long long)s * a.hk + head) * a.cap + pos;
+  crow = ((long long)s * a.hk + sl.head) * a.cap + pos;
   return true;
 }
 
-// The e4m3 bits nearest to amax / 6, ties to even, at most 448, from the unrounded quotient: the
-// quotient truncated to fp32 takes a set last bit when it is not exact, so that the second
-// rounding sees which side of a midpoint it is on.
+// Two values to the nearest e4m3 codes, at most 448: a in the low byte.
+__device__ __forceinline__ uint32_t e4m3x2_from_f32(float a, float b) {
+  unsigned short r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+// The e4m3 bits nearest to amax / 6, ties to even, at most 448, from the unrounded quotient.  That is
+// bracketed: the product with 1 / 6, both rounded towards 0, is at most 2^-22 below it, so 4 units in
+// the last place more are at least it.  Where a midpoint lies between the ends the quotient truncated
+// to fp32 takes a set last bit if it is not exact, so that the second rounding sees its side.
 __device__ __forceinline__ uint32_t q4_scale(float amax) {
   const float c = fminf(amax, 6.f * 448.f);
-  float t = __fdiv_rz(c, 6.f);
-  if (fmaf(-6.f, t, c) != 0.f) t = __uint_as_float(__float_as_uint(t) | 1u);
-  unsigned short r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(t));
+  const float lo = __fmul_rz(c, __uint_as_float(0x3e2aaaaau));
+  uint32_t r = e4m3x2_from_f32(lo, __uint_as_float(__float_as_uint(lo) + 4u));
+  if ((r & 0xffu) != r >> 8) {
+    float t = __fdiv_rz(c, 6.f);
+    if (fmaf(-6.f, t, c) != 0.f) t = __uint_as_float(__float_as_uint(t) | 1u);
+    r = e4m3x2_from_f32(t, t);
+  }
   return r & 0x7fu;
 }
 
 // The e2m1 code nearest to |y| / s, ties to the even code: a binary search of the midpoints
-// 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5, each times s exact in fp32.
+// 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5, each times s exact in fp32.  NaN gives 0.
 __device__ __forceinline__ uint32_t q4_code(float y, float s) {
   const float a = fabsf(y);
   const bool b2 = a >= 1.75f * s;
@@ -95,41 +119,81 @@ __device__ __forceinline__ uint32_t q4_code(float y, float s) {
   return c;
 }
 
+// Eight values to the nearest e2m1 codes, the first in the low nibble.
+__device__ __forceinline__ uint32_t e2m1x8_from_f32(const float (&q)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(r)
+      : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+  return r;
+}
+
+// The codes of 8 values y under scale s > 0, the quotient bracketed again: 1 / s to one unit in the
+// last place, less two, is at most 3 units below it, and the truncated product at most 2^-21 below the
+// quotient, so 8 units more are at least it.  Where both ends have the same codes those are the
+// quotient's; elsewhere (a midpoint between the ends: ~2e-6 of random values, exact ties) the
+// comparisons decide.  So they do for a NaN, whose upper end wraps round to a tiny value and code 0,
+// and for a negative infinity, whose upper end is a NaN and takes the largest positive code.
+__device__ __forceinline__ uint32_t q4_codes(const float (&y)[8], float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  r = __uint_as_float(__float_as_uint(r) - 2u);
+  float lo[8], hi[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    lo[e] = __fmul_rz(y[e], r);
+    hi[e] = __uint_as_float(__float_as_uint(lo[e]) + 8u);
+  }
+  uint32_t c = e2m1x8_from_f32(lo);
+  if (c != e2m1x8_from_f32(hi)) {
+    c = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c |= q4_code(y[e], s) << (4 * e);
+    return c;
+  }
+  const uint32_t some = (c | c >> 1 | c >> 2) & 0x11111111u;  // a code of 0 has no sign
+  return c & (0x77777777u | some << 3);
+}
+
 // Quantises this thread's 8 dims of one side; its partner (lane xor 1) holds the other 8 of the
 // scale's 16.  All lanes of the warp take part in the exchange.
-__device__ __forceinline__ void q4_quantise(const float4& x0, const float4& x1, float inv, bool on,
+__device__ __forceinline__ void q4_quantise(const float4& x0, const float4& x1, float inv,
                                             uint32_t& codes, uint32_t& scale) {
-  float y[8] = {x0.x * inv, x0.y * inv, x0.z * inv, x0.w * inv,
-                x1.x * inv, x1.y * inv, x1.z * inv, x1.w * inv};
+  const float y[8] = {x0.x * inv, x0.y * inv, x0.z * inv, x0.w * inv,
+                      x1.x * inv, x1.y * inv, x1.z * inv, x1.w * inv};
   float amax = 0.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(y[e]));  // fmaxf drops a NaN
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  scale = on ? q4_scale(amax) : 0u;
-  codes = 0;
-  if (!scale) return;
-  const float s = e4m3_to_f32(scale);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) codes |= q4_code(y[e], s) << (4 * e);
+  scale = q4_scale(amax);
+  codes = scale ? q4_codes(y, e4m3_to_f32(scale)) : 0u;
 }
 
 template <int D>
-__global__ void __launch_bounds__(kQ4Threads)
+__global__ void __launch_bounds__(kQ4Threads<D, 8, kRowBlock>)
     append_q4_kernel(const float* __restrict__ k_new, const float* __restrict__ v_new, Q4Rows a) {
-  long long elem = 0, crow = 0;
-  int slice = 0;
-  const bool on = q4_place<D>(a, elem, crow, slice);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const Q4Slot sl = q4_slot<D, 8>(a, 0);
   float4 k0{}, k1{}, v0{}, v1{};
-  if (on) {
-    k0 = __ldg(reinterpret_cast<const float4*>(k_new + elem));
-    k1 = __ldg(reinterpret_cast<const float4*>(k_new + elem) + 1);
-    v0 = __ldg(reinterpret_cast<const float4*>(v_new + elem));
-    v1 = __ldg(reinterpret_cast<const float4*>(v_new + elem) + 1);
+  if (sl.r < a.n_rows) {
+    k0 = __ldcs(reinterpret_cast<const float4*>(k_new + sl.elem));
+    k1 = __ldcs(reinterpret_cast<const float4*>(k_new + sl.elem) + 1);
+    v0 = __ldcs(reinterpret_cast<const float4*>(v_new + sl.elem));
+    v1 = __ldcs(reinterpret_cast<const float4*>(v_new + sl.elem) + 1);
   }
+  long long crow = 0;
+  const bool on = q4_place<D, 8>(a, sl, crow);
   uint32_t kc, ks, vc, vs;
-  q4_quantise(k0, k1, a.k_scale, on, kc, ks);
-  q4_quantise(v0, v1, a.v_scale, on, vc, vs);
+  q4_quantise(k0, k1, a.k_scale, kc, ks);
+  q4_quantise(v0, v1, a.v_scale, vc, vs);
   if (!on) return;
+  const int slice = threadIdx.x % (D / 8);
   *reinterpret_cast<uint32_t*>(a.kq + crow * (D / 2) + slice * 4) = kc;
   *reinterpret_cast<uint32_t*>(a.vq + crow * (D / 2) + slice * 4) = vc;
   if ((slice & 1) == 0) {
@@ -138,49 +202,73 @@ __global__ void __launch_bounds__(kQ4Threads)
   }
 }
 
-// 8 codes times scale s -> 8 values.
-__device__ __forceinline__ void q4_values(uint32_t codes, float s, float (&f)[8]) {
+// A thread's rows in reading: f16 8 dims of a row, fp32 4 dims of two rows 8 apart.
+template <typename T>
+constexpr int kReadDims = sizeof(T) == 4 ? 4 : 8;
+template <typename T>
+constexpr int kReadRows = sizeof(T) == 4 ? 8 : kRowBlock;
+
+// The codes of a thread's dims, and their values times s, stored.
+template <typename T>
+__device__ __forceinline__ uint32_t q4_load(const uint8_t* src) {
+  if constexpr (sizeof(T) == 4)
+    return __ldg(reinterpret_cast<const uint16_t*>(src));
+  else
+    return __ldg(reinterpret_cast<const uint32_t*>(src));
+}
+template <typename T>
+__device__ __forceinline__ void q4_store(T* dst, uint32_t codes, float s) {
   uint32_t h[4];
   e2m1x8_to_f16x2(codes, h);
+  float2 x[4];
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
-    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h[b]));
-    f[2 * b] = x.x * s;
-    f[2 * b + 1] = x.y * s;
+    x[b] = __half22float2(*reinterpret_cast<const __half2*>(&h[b]));
+    x[b].x *= s;
+    x[b].y *= s;
   }
-}
-
-template <typename T>
-__device__ __forceinline__ void q4_store(T* dst, const float (&f)[8]) {
   if constexpr (sizeof(T) == 4) {
-    reinterpret_cast<float4*>(dst)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(dst)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    __stcs(reinterpret_cast<float4*>(dst), make_float4(x[0].x, x[0].y, x[1].x, x[1].y));
   } else {
     union {
-      __half2 h[4];
+      __half2 h2[4];
       uint4 u;
     } o;
 #pragma unroll
-    for (int b = 0; b < 4; ++b) o.h[b] = __floats2half2_rn(f[2 * b], f[2 * b + 1]);
-    *reinterpret_cast<uint4*>(dst) = o.u;
+    for (int b = 0; b < 4; ++b) o.h2[b] = __floats2half2_rn(x[b].x, x[b].y);
+    __stcs(reinterpret_cast<uint4*>(dst), o.u);
   }
 }
 
 template <int D, typename T>
-__global__ void __launch_bounds__(kQ4Threads)
+__global__ void __launch_bounds__(kQ4Threads<D, kReadDims<T>, kReadRows<T>>)
     read_q4_kernel(T* __restrict__ k_out, T* __restrict__ v_out, Q4Rows a) {
-  long long elem = 0, crow = 0;
-  int slice = 0;
-  if (!q4_place<D>(a, elem, crow, slice)) return;
-  const uint32_t kc = __ldg(reinterpret_cast<const uint32_t*>(a.kq + crow * (D / 2)) + slice);
-  const uint32_t vc = __ldg(reinterpret_cast<const uint32_t*>(a.vq + crow * (D / 2)) + slice);
-  const uint32_t ks = __ldg(a.ksc + crow * (D / 16) + slice / 2);
-  const uint32_t vs = __ldg(a.vsc + crow * (D / 16) + slice / 2);
-  float f[8];
-  q4_values(kc, e4m3_to_f32(ks) * a.k_scale, f);
-  q4_store(k_out + elem, f);
-  q4_values(vc, e4m3_to_f32(vs) * a.v_scale, f);
-  q4_store(v_out + elem, f);
+  constexpr int DPT = kReadDims<T>, N = kRowBlock / kReadRows<T>;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int slice = threadIdx.x % (D / DPT);
+  Q4Slot sl[N];
+  bool on[N];
+  uint32_t kc[N], vc[N], ks[N], vs[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    sl[j] = q4_slot<D, DPT>(a, j * kReadRows<T>);
+    long long crow = 0;
+    on[j] = q4_place<D, DPT>(a, sl[j], crow);
+    kc[j] = vc[j] = ks[j] = vs[j] = 0;
+    if (on[j]) {
+      kc[j] = q4_load<T>(a.kq + crow * (D / 2) + slice * (DPT / 2));
+      vc[j] = q4_load<T>(a.vq + crow * (D / 2) + slice * (DPT / 2));
+      ks[j] = __ldg(a.ksc + crow * (D / 16) + slice * DPT / 16);
+      vs[j] = __ldg(a.vsc + crow * (D / 16) + slice * DPT / 16);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+    if (on[j]) {
+      q4_store(k_out + sl[j].elem, kc[j], e4m3_to_f32(ks[j]) * a.k_scale);
+      q4_store(v_out + sl[j].elem, vc[j], e4m3_to_f32(vs[j]) * a.v_scale);
+    }
 }
 
 bool q4_scale_ok(float s) {
@@ -213,15 +301,25 @@ gqa_status q4_rows_call(const char* name, const Q4Rows& a, int head_dim, const v
     return bad(GQA_EINVAL, "the rows, codes and scales must be 16-byte aligned");
   if ((bits(a.row_off) | bits(a.t0) | bits(a.err)) & 3)
     return bad(GQA_EINVAL, "row_off, t0 and err_word must be 4-byte aligned");
-  const long long blocks_of_rows = (a.n_rows + (long long)kRowBlock - 1) / kRowBlock;
-  if (blocks_of_rows * a.hk > (1LL << 40))
-    return bad(GQA_EUNSUPPORTED, "too many rows for one launch");
-  const long long threads = blocks_of_rows * kRowBlock * a.hk * (head_dim / 8);
-  const long long blocks = (threads + kQ4Threads - 1) / kQ4Threads;
+  const long long blocks = (a.n_rows + (long long)kRowBlock - 1) / kRowBlock * a.hk;
   if (blocks > 0x7fffffffLL) return bad(GQA_EUNSUPPORTED, "too many rows for one launch");
-  go(static_cast<unsigned>(blocks));
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? GQA_OK : bad(GQA_ECUDA, cudaGetErrorString(e));
+  const cudaError_t e = go(static_cast<unsigned>(blocks));
+  if (e == cudaSuccess) return GQA_OK;
+  (void)cudaGetLastError();
+  return bad(GQA_ECUDA, cudaGetErrorString(e));
+}
+
+// A launch whose scheduling overlaps the end of the kernel before it on the stream.
+template <class Kern, class... Args>
+cudaError_t q4_launch(Kern kern, unsigned blocks, int threads, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  cfg.attrs = at;
+  cfg.numAttrs = cluster_attrs(at, 0, 1);
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 }  // namespace gqa
@@ -237,12 +335,12 @@ extern "C" gqa_status kv_append_q4(const float* k_new, const float* v_new, int n
     gqa::Q4Rows b = a;
     b.k_scale = 1.f / k_scale;
     b.v_scale = 1.f / v_scale;
+    using namespace gqa;
     if (head_dim == 64)
-      gqa::append_q4_kernel<64><<<blocks, gqa::kQ4Threads, 0, stream>>>(k_new, v_new, b);
-    else if (head_dim == 128)
-      gqa::append_q4_kernel<128><<<blocks, gqa::kQ4Threads, 0, stream>>>(k_new, v_new, b);
-    else
-      gqa::append_q4_kernel<256><<<blocks, gqa::kQ4Threads, 0, stream>>>(k_new, v_new, b);
+      return q4_launch(append_q4_kernel<64>, blocks, kQ4Threads<64, 8, kRowBlock>, stream, k_new, v_new, b);
+    if (head_dim == 128)
+      return q4_launch(append_q4_kernel<128>, blocks, kQ4Threads<128, 8, kRowBlock>, stream, k_new, v_new, b);
+    return q4_launch(append_q4_kernel<256>, blocks, kQ4Threads<256, 8, kRowBlock>, stream, k_new, v_new, b);
   });
 }
 
@@ -256,19 +354,18 @@ extern "C" gqa_status kv_read_q4(const uint8_t* kq, const uint8_t* vq, const uin
                 const_cast<uint8_t*>(ksc), const_cast<uint8_t*>(vsc),
                 row_off, t0, err_word, n_rows, n_kv_heads, n_seq, cache_cap, k_scale, v_scale};
   return gqa::q4_rows_call("kv_read_q4", a, head_dim, k_out, v_out, [&](unsigned blocks) {
-    auto launch = [&](auto kern32, auto kern16) {
-      if (out_f16)
-        kern16<<<blocks, gqa::kQ4Threads, 0, stream>>>(static_cast<__half*>(k_out),
-                                                       static_cast<__half*>(v_out), a);
-      else
-        kern32<<<blocks, gqa::kQ4Threads, 0, stream>>>(static_cast<float*>(k_out),
-                                                       static_cast<float*>(v_out), a);
+    using namespace gqa;
+    auto launch = [&](auto d) {
+      constexpr int D = decltype(d)::value;
+      return out_f16 ? q4_launch(read_q4_kernel<D, __half>, blocks,
+                                 kQ4Threads<D, kReadDims<__half>, kReadRows<__half>>, stream,
+                                 static_cast<__half*>(k_out), static_cast<__half*>(v_out), a)
+                     : q4_launch(read_q4_kernel<D, float>, blocks,
+                                 kQ4Threads<D, kReadDims<float>, kReadRows<float>>, stream,
+                                 static_cast<float*>(k_out), static_cast<float*>(v_out), a);
     };
-    if (head_dim == 64)
-      launch(gqa::read_q4_kernel<64, float>, gqa::read_q4_kernel<64, __half>);
-    else if (head_dim == 128)
-      launch(gqa::read_q4_kernel<128, float>, gqa::read_q4_kernel<128, __half>);
-    else
-      launch(gqa::read_q4_kernel<256, float>, gqa::read_q4_kernel<256, __half>);
+    if (head_dim == 64) return launch(std::integral_constant<int, 64>());
+    if (head_dim == 128) return launch(std::integral_constant<int, 128>());
+    return launch(std::integral_constant<int, 256>());
   });
 }

@@ -795,12 +795,17 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D, PN, NW>::NW, Q4Cfg<D, PN, NW>::M
   }
 }
 
-// Clusters of n CTAs of this kernel that the GPU holds at once (asked once per size); 0 where the
-// size is not to be had.  More than 8 CTAs a cluster need the function's consent.
+// Clusters of n CTAs of this kernel that the GPU holds at once (asked once per size and device); 0
+// where the size is not to be had.  More than 8 CTAs a cluster need the function's consent.
 template <int D, int PN, int NW>
 static int clusters_at_once(cudaLaunchConfig_t cfg, unsigned n) {
-  static std::atomic<int> known[kQ4MaxCluster + 1];  // 1 + the number
-  if (n < 2 || n > static_cast<unsigned>(kQ4MaxCluster)) return 0;
+  constexpr int kDevices = 32;
+  static std::atomic<int> known_of[kDevices][kQ4MaxCluster + 1];  // 1 + the number
+  int dev = 0;
+  if (n < 2 || n > static_cast<unsigned>(kQ4MaxCluster) || cudaGetDevice(&dev) != cudaSuccess ||
+      dev < 0 || dev >= kDevices)
+    return 0;
+  auto& known = known_of[dev];
   if (known[n].load() == 0) {
     const void* fn = reinterpret_cast<const void*>(&q4_mma_kernel<D, PN, NW>);
     cudaLaunchAttribute at[1];

@@ -84,7 +84,7 @@ gqa_status plan_visible(int n_tok, int n_seq, int n_heads, int n_kv_heads, int h
   while (q4 && (group % hs || group / hs > 8)) ++hs;
   const int tile = q4 ? q4_tile(head_dim) : stage_rows(GQA_KIND_F16, head_dim);
   // the sinks' last tile and the window's last one (4-bit: its first one too) are partly seen
-  const long long tiles = (n + tile - 1) / tile + (budget > 0 ? 2 : 0);
+  const long long tiles = std::max(1LL, (n + tile - 1) / tile + (budget > 0 ? 2 : 0));
   // 4-bit rows that may share a sequence: as many a CTA as their heads leave room for
   const int rows = q4 && n_seq < n_tok ? 8 / (group / hs) : 1;
   const long long groups = (n_tok + rows - 1) / rows;
@@ -103,8 +103,8 @@ gqa_status plan_visible(int n_tok, int n_seq, int n_heads, int n_kv_heads, int h
     chunk = (forced + tile - 1) / tile;
   } else if (q4 && !big && units <= num_sms) {
     // one CTA of eight warps an SM, a tile a warp at the least, at most 16 chunks a row (a cluster)
-    const long long most = std::min<long long>(std::min<long long>(num_sms / units, kQ4MaxCluster),
-                                               std::max(1LL, tiles / 8));
+    const long long most = std::min(std::min<long long>(num_sms / units, kQ4MaxCluster),
+                                    std::max(1LL, tiles / 8));
     chunk = (tiles + most - 1) / most;
   } else if (!q4 && chunk < tiles) {
     // a split grid that fits the GPU merges each row in a cluster of up to 8 chunk CTAs
@@ -112,8 +112,8 @@ gqa_status plan_visible(int n_tok, int n_seq, int n_heads, int n_kv_heads, int h
     if (units * ((tiles + c8 - 1) / c8) <= num_sms) chunk = c8;
   }
   if (q4) chunk = std::max(chunk, (tiles + kQ4MaxSplit - 1) / kQ4MaxSplit);
-  chunk = std::min(chunk, std::max(tiles, 1LL));
-  const long long n_split = std::max(1LL, (tiles + chunk - 1) / chunk);
+  chunk = std::min(chunk, tiles);
+  const long long n_split = (tiles + chunk - 1) / chunk;
   if (n_split > (1 << 30) || (long long)n_kv_heads * hs > 65535)
     return fail(GQA_EUNSUPPORTED, "too many chunks or heads for one launch");
   const char* fc = std::getenv("GQA_FORCE_CTAS");  // tests: a balanced grid of this many

@@ -292,6 +292,59 @@ def test_decode_nan_query(chunk):
     assert_close(got, ref, TOL, "NaN query")
 
 
+def test_decode_over_nothing_and_tiny_caches():
+    """max_kv_len 0, no rows, and caches of 16 positions under many rows."""
+    rng = np.random.default_rng(15)
+    cache = q4_cache(rng, [16], 2, 16, 128)
+    q = rows(rng, 200, 8, 128)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = run_q4(q[:1], cache, [0], max_kv_len=0, err=err)
+    assert (got == 0).all() and int(err) == 0
+    assert run_q4(q[:0], cache, []).shape == (0, 8, 128)
+    lens = [int(n) for n in rng.integers(0, 17, 200)]
+    for env in ("on", "off"):
+        with _env(GQA_Q4_ROWS=env):
+            got = run_q4(q, cache, lens, [0] * 200, err=err).cpu().numpy()
+        assert_close(got, oracle.decode_q4(q, *cache, lens, 128 ** -0.5, seq_of=[0] * 200), TOL, env)
+    assert int(err) == 0
+
+
+def test_first_call_is_captured():
+    """A fresh process whose first call of each kernel is inside a capture."""
+    import subprocess
+    import sys
+    code = """
+import torch
+from gqa_decode_attention_03_gb300 import gqa_decode as gd
+z = lambda *s: torch.zeros(s, dtype=torch.uint8, device="cuda")
+i = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+cache = [z(1, 8, 8192, 64), z(1, 8, 8192, 64), z(1, 8, 8192, 8), z(1, 8, 8192, 8)]
+k = torch.ones(40, 8, 128, device="cuda")
+q, out = torch.ones(40, 32, 128, device="cuda"), torch.zeros(40, 32, 128, device="cuda")
+f = torch.ones(1, 8192, 8, 128, dtype=torch.float16, device="cuda")
+off, t0, n, s = i(0, 40), i(0), i(*[40] * 40), i(*[0] * 40)
+ws = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+outs = [torch.zeros_like(out) for _ in range(4)]
+with torch.cuda.graph(g):
+    gd.kv_append_q4(k, k, *cache, off, t0)
+    gd.attn_decode_q4(q[:1], *cache, n[:1], out=outs[0][:1], ws=ws)
+    gd.attn_decode_q4(q, *cache, n, seq_of=s, out=outs[1], ws=ws)
+    gd.attn_decode_f16_window(q[:1], f, f, n[:1], 5000, 4, out=outs[2][:1], ws=ws)
+    gd.attn_decode_f16_window(q, f, f, n, 30, 4, seq_of=s, out=outs[3], ws=ws)
+g.replay()
+torch.cuda.synchronize()
+v = gd.kv_read_q4(*cache, off, t0, n_rows=40)[1][0, 0, 0].item()  # 1 = code x scale e4m3(1 / 6)
+assert abs(v - 1) < 0.1
+for o, rows, x in zip(outs, (1, 40, 1, 40), (v, v, 1, 1)):
+    assert (o[:rows] - x).abs().max().item() < 1e-4, (rows, x)
+print("fine")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
+
+
 def test_decode_bad_lengths_and_sequences():
     gd = _gd()
     rng = np.random.default_rng(5)

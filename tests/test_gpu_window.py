@@ -200,6 +200,21 @@ def test_large_scores_and_infinite_values_in_sight():
     assert not np.isfinite(got[0, :, 3]).any() and np.isfinite(np.delete(got, 3, 2)).all()
 
 
+def test_tiny_caches_under_many_rows():
+    rng = np.random.default_rng(15)
+    for D in (64, 128):
+        k, v = f16_cache(rng, 1, 9, 2, D)
+        q = rows(rng, 200, 8, D)
+        lens = [int(n) for n in rng.integers(0, 10, 200)]
+        got = run(q, k, v, lens, 5, 2, [0] * 200).cpu().numpy()
+        ref = oracle.decode_f16_window(q, k, v, lens, D ** -0.5, 5, 2, seq_of=[0] * 200)
+        assert_close(got, ref, TOL, f"D {D}")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = run(q[:1], k, v, [0], 5, 2, max_kv_len=0, err=err)
+    assert (got == 0).all() and int(err) == 0
+    assert run(q[:0], k, v, [], 5, 2).shape == (0, 8, 128)
+
+
 def test_bad_lengths_and_sequences():
     gd = _gd()
     rng = np.random.default_rng(5)

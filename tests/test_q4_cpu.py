@@ -192,3 +192,45 @@ def test_plans_check_their_sizes(gd):
         with pytest.raises(gd.GqaError, match="EINVAL"):
             gd.plan(1, 4, 1, 32, 10, 5, kind, num_sms=152)             # head_dim 32
         assert gd.plan(1, 4, 1, 64, 0, 5, kind, num_sms=152).merge == 0
+        for n_tok, n_seq in ((0, 1), (1, 1), (300, 1), (300, 300)):
+            p = gd.plan(n_tok, 32, 8, 128, 0, kind=kind, num_sms=152, n_seq=n_seq)
+            assert p.merge == 0 and p.ws_bytes == 0
+
+
+def test_q4_plans(gd):
+    def plan(n_tok, H, Hk, D, n, budget=-1, n_seq=None):
+        return gd.plan(n_tok, H, Hk, D, n, budget, gd.KIND_Q4, num_sms=152, n_seq=n_seq)
+
+    # a ragged batch of long rows: one wave of three CTAs an SM with equal shares; counters, then two
+    # records of the group's 4 heads a CTA
+    p = plan(16, 32, 8, 128, 32768)
+    assert p.streamk == 1 and (p.grid_x, p.grid_y, p.grid_z) == (456, 1, 1)
+    assert p.ws_bytes == 512 + 2 * 456 * 4 * 130 * 4
+    # short lists, or more rows than the shares are found for: chunks of 2048 positions
+    p = plan(64, 32, 8, 128, 8192)
+    assert p.streamk == 0 and p.chunk == 2048 and (p.grid_x, p.grid_y, p.grid_z) == (4, 8, 64)
+    assert plan(300, 32, 8, 128, 32768).streamk == 0
+    # one row: as many chunks as give every SM one CTA, at most 16
+    p = plan(1, 48, 4, 256, 8191)
+    assert p.n_split == 16 and p.grid_y == 8 and p.chunk == 512     # 12 heads: two CTAs of 6
+    assert plan(1, 4, 1, 64, 256).merge == 0
+    # rows that may share a sequence: two of four heads a CTA, 128 / 4 where there is work enough
+    assert plan(32, 32, 8, 64, 8100, 2052, n_seq=2).row_group == 2
+    p = plan(512, 32, 8, 128, 8000, n_seq=1)
+    assert p.row_group == 32 and (p.grid_x, p.grid_y, p.grid_z) == (1, 8, 16) and p.merge == 0
+    assert plan(64, 32, 8, 128, 8000, n_seq=1).n_split == 9
+    assert plan(512, 32, 8, 256, 8000, n_seq=1).row_group == 2      # head_dim 256
+
+
+def test_f16_window_plans(gd, monkeypatch):
+    def plan(n_tok, H, Hk, D, n, budget, n_seq=None):
+        return gd.plan(n_tok, H, Hk, D, n, budget, gd.KIND_F16_WINDOW, num_sms=152, n_seq=n_seq)
+
+    # what a row sees sizes the grid: 1024 + 4 positions, in a cluster of up to 8 chunks
+    p = plan(1, 32, 8, 64, 16001, 1028)
+    assert p.tile == 128 and p.n_split == 6 and p.merge == 1
+    # a chunk of a prompt: 128 pairs a CTA
+    p = plan(512, 32, 8, 128, 6500, 2064, n_seq=1)
+    assert p.row_group == 32 and p.grid_z == 16 and p.merge == 0
+    monkeypatch.setenv("GQA_F16_ROWS", "off")
+    assert plan(512, 32, 8, 128, 6500, 2064, n_seq=1).row_group == 1
