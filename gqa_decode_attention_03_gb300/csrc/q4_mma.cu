@@ -2,7 +2,7 @@
 //
 // A CTA works on a piece of the list of tiles that a (group of rows, KV head x head split) sees: a
 // chunk of it, one a CTA, or, where that would take several waves of long chunks, an equal share of
-// all lists end to end (the 16-row ragged batch: 63.4 us against 69.8).  Each of its four warps
+// all lists end to end (the 16-row ragged batch: 59.3 us against 69.8).  Each of its four warps
 // streams every fourth tile of the piece through a ring of its own and keeps its own running
 // maximum, sum and accumulator, so nothing but the end of the piece synchronises the CTA.  A tile
 // is TP positions of one KV head: four contiguous runs of the head-major cache (codes and scales of
@@ -647,8 +647,8 @@ __device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const
     return;
   }
 
-  // ---- the last CTA of the pieces (a ticket; nobody waits) merges them by log-sum-exp: a warp
-  //      finds a pair's weights, then the threads fold the pieces' records, 16 loads in flight
+  // ---- the last CTA of the pieces (a ticket; nobody waits) merges them by log-sum-exp: a few pieces
+  //      at once, many by weights that a warp finds for a pair and loads of 16 pieces at a time
   __shared__ int s_last;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -659,6 +659,37 @@ __device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const
   __syncthreads();
   if (!s_last) return;
   __threadfence();
+  constexpr int TPP = D / 2;  // threads of a pair, two dims each
+  static_assert((32 * C::NW) % TPP == 0, "whole pairs a pass");
+  const int d = 2 * (threadIdx.x % TPP);
+  if (pieces <= kQ4FewPieces) {  // every thread on its own: all loads of its dims in one round trip
+    for (int h = threadIdx.x / TPP; h < np; h += 32 * C::NW / TPP) {
+      const int row = h / G, t = t0 + row, head = head0 + h - row * G;
+      const float* src = record(h, t, head);
+      float2 ml[kQ4FewPieces], v[kQ4FewPieces];
+#pragma unroll
+      for (int k = 0; k < kQ4FewPieces; ++k) {  // past the last piece: the last one again, no weight
+        const float* r = src + (min(k, pieces - 1) ? min(k, pieces - 1) * rec : rec0);
+        ml[k] = __ldcg(reinterpret_cast<const float2*>(r + D));
+        v[k] = __ldcg(reinterpret_cast<const float2*>(r + d));
+      }
+      float M = -INFINITY, Ls = 0.f;
+#pragma unroll
+      for (int k = 0; k < kQ4FewPieces; ++k) M = fmaxf(M, ml[k].x);
+      float2 a = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kQ4FewPieces; ++k) {
+        const float e = k >= pieces || ml[k].x == -INFINITY ? 0.f : __expf(ml[k].x - M);
+        Ls = fmaf(ml[k].y, e, Ls);
+        a.x = fmaf(v[k].x, e, a.x);
+        a.y = fmaf(v[k].y, e, a.y);
+      }
+      const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
+      *reinterpret_cast<float2*>(p.out + ((size_t)t * p.n_heads + head) * D + d) =
+          make_float2(gated(p, t, head, d, a.x * inv), gated(p, t, head, d + 1, a.y * inv));
+    }
+    return;
+  }
   float* wt = reinterpret_cast<float*>(smem);  // [pair][pieces]
   for (int h = warp; h < np; h += C::NW) {
     const int row = h / G;
@@ -681,9 +712,6 @@ __device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const
     }
   }
   __syncthreads();
-  constexpr int TPP = D / 2;  // threads of a pair, two dims each
-  static_assert((32 * C::NW) % TPP == 0, "whole pairs a pass");
-  const int d = 2 * (threadIdx.x % TPP);
   for (int h = threadIdx.x / TPP; h < np; h += 32 * C::NW / TPP) {
     const int row = h / G, t = t0 + row, head = head0 + h - row * G;
     const float* src = record(h, t, head) + d;
@@ -725,8 +753,9 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D, PN, NW>::NW, Q4Cfg<D, PN, NW>::M
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   uint32_t phases = 0;  // the parity each stage's next wait is for
-  // Balanced: one wave of CTAs, each with an equal share of all rows' tiles end to end (row by row,
-  // column by column).  s_pre: the rows' tiles added up.  What the loop goes by stays in shared
+  // Balanced: one wave of CTAs, each with an equal share of all rows' lists end to end (row by row,
+  // column by column), a list counted as its tiles and kQ4ListCost more ahead of them for its start
+  // and end.  s_pre: the rows' counts added up.  What the loop goes by stays in shared
   // memory: one copy of q4_item, with no more alive around it than the chunks of a grid need.
   __shared__ long long s_f, s_end, s_per;
   const int n_tok = p.n_tok, U = qp.columns, b = blockIdx.x;
@@ -735,7 +764,8 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D, PN, NW>::NW, Q4Cfg<D, PN, NW>::M
       int seq;
       const Visible v(visible_row(p, r, b == 0, seq), p.window, p.n_sink);
       const int base = (v.w0 & ~15) <= v.ns ? 0 : v.w0 & ~15, ns = base ? v.ns : 0;
-      s_pre[r + 1] = (ns + C::TP - 1) / C::TP + (v.L - base + C::TP - 1) / C::TP;
+      const int tiles = (ns + C::TP - 1) / C::TP + (v.L - base + C::TP - 1) / C::TP;
+    s_pre[r + 1] = tiles ? tiles + kQ4ListCost : 0;
     }
     if (threadIdx.x == 0) s_pre[0] = 0;
     __syncthreads();
@@ -774,19 +804,25 @@ __global__ void __launch_bounds__(32 * Q4Cfg<D, PN, NW>::NW, Q4Cfg<D, PN, NW>::M
       int z = 0;  // the last row that starts at or before f
       for (int step = kQ4BalancedRows / 2; step; step /= 2)
         if (z + step < n_tok && (long long)U * s_pre[z + step] <= f) z += step;
-      const int n = s_pre[z + 1] - s_pre[z];
+      const int n = s_pre[z + 1] - s_pre[z];  // its columns' lists: kQ4ListCost + tiles
       const int off = static_cast<int>(f - (long long)U * s_pre[z]);
       it.z = z;
       it.y = off / n;
-      it.a = off - it.y * n;
-      it.b = static_cast<int>(min((long long)n, it.a + (s_end - f)));
-      const long long start = f - it.a;  // of the row's column
+      const int a = off - it.y * n;
+      const int b2 = static_cast<int>(min((long long)n, a + (s_end - f)));
+      const long long start = f - a + kQ4ListCost;  // where the list's tiles start
       const int c0 = static_cast<int>(start / per);
-      it.pieces = static_cast<int>((start + n - 1) / per) - c0 + 1;
+      it.a = max(a - kQ4ListCost, 0);
+      it.b = max(b2 - kQ4ListCost, 0);
+      it.pieces = static_cast<int>((start + n - kQ4ListCost - 1) / per) - c0 + 1;
       it.piece = b - c0;
       it.slot = 2 * c0;
       __syncthreads();
-      if (threadIdx.x == 0) s_f = f + (it.b - it.a);
+      if (threadIdx.x == 0) s_f = f + (b2 - a);
+      if (it.b == 0) {  // none of its tiles yet
+        __syncthreads();
+        continue;
+      }
     }
     q4_item<D, PN, NW>(qp, smem, it, phases);
     if (!qp.balanced) return;

@@ -207,9 +207,10 @@ def test_q4_plans(gd):
     assert p.streamk == 1 and (p.grid_x, p.grid_y, p.grid_z) == (456, 1, 1)
     assert p.ws_bytes == 512 + 2 * 456 * 4 * 130 * 4
     # short lists, or more rows than the shares are found for: chunks of 2048 positions
-    p = plan(64, 32, 8, 128, 8192)
-    assert p.streamk == 0 and p.chunk == 2048 and (p.grid_x, p.grid_y, p.grid_z) == (4, 8, 64)
-    assert plan(300, 32, 8, 128, 32768).streamk == 0
+    p = plan(200, 32, 8, 128, 1024)
+    assert p.streamk == 0 and p.merge == 0 and (p.grid_x, p.grid_y, p.grid_z) == (1, 8, 200)
+    p = plan(300, 32, 8, 128, 32768)
+    assert p.streamk == 0 and p.chunk == 2048 and (p.grid_x, p.grid_y, p.grid_z) == (16, 8, 300)
     # one row: as many chunks as give every SM one CTA, at most 16
     p = plan(1, 48, 4, 256, 8191)
     assert p.n_split == 16 and p.grid_y == 8 and p.chunk == 512     # 12 heads: two CTAs of 6
