@@ -40,8 +40,9 @@ constexpr long long kQ4RowsMinWork = 3LL << 20;
 // n: positions a row sees at most.
 static bool rows_grouped(bool q4, int n_tok, int n_seq, int n_heads, int group, int head_dim,
                          long long n) {
+  if (head_dim == 256 || n_seq >= n_tok) return false;
   const char* r = std::getenv(q4 ? "GQA_Q4_ROWS" : "GQA_F16_ROWS");
-  if (head_dim == 256 || n_seq >= n_tok || (r && std::strcmp(r, "off") == 0)) return false;
+  if (r && std::strcmp(r, "off") == 0) return false;
   if (r && std::strcmp(r, "on") == 0) return true;  // tests, comparison
   return (long long)n_tok * group >= (long long)kRowsMinPairs * n_seq &&
          (!q4 || (long long)n_tok * n_heads * n >= kQ4RowsMinWork);
@@ -116,10 +117,10 @@ gqa_status plan_visible(int n_tok, int n_seq, int n_heads, int n_kv_heads, int h
   const long long n_split = (tiles + chunk - 1) / chunk;
   if (n_split > (1 << 30) || (long long)n_kv_heads * hs > 65535)
     return fail(GQA_EUNSUPPORTED, "too many chunks or heads for one launch");
-  const char* fc = std::getenv("GQA_FORCE_CTAS");  // tests: a balanced grid of this many
+  const bool can_balance = q4 && rows == 1 && n_tok <= kQ4BalancedRows && forced <= 0;
+  const char* fc = can_balance ? std::getenv("GQA_FORCE_CTAS") : nullptr;  // tests: CTAs of the wave
   const int forced_ctas = fc ? std::atoi(fc) : 0;
-  if (q4 && rows == 1 && n_tok <= kQ4BalancedRows && forced <= 0 &&
-      (forced_ctas > 0 || (big && n >= kQ4LongList))) {
+  if (can_balance && (forced_ctas > 0 || (big && n >= kQ4LongList))) {
     const long long ctas = forced_ctas > 0 ? std::min(forced_ctas, 65535) : slots;
     plan->n_split = plan->grid_x = (int)ctas;
     plan->grid_y = plan->grid_z = 1;
