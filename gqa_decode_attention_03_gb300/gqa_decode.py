@@ -8,6 +8,7 @@ fallback of any kind: importing this module raises if the library has not been b
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from pathlib import Path
@@ -411,6 +412,18 @@ def _refuse(x, dtype, name, device, ndim=None):
         raise ValueError(f"{name} is on cuda:{x.get_device()}, the current device is cuda:{device}")
 
 
+def _making(stream, device):
+    """Where a call makes its own outputs and workspace: on the stream that it runs on, so that their
+    zeros are not written late nor their memory given away early."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
+    if stream.device.index != device:
+        raise ValueError(f"the stream is on {stream.device}, the current device is cuda:{device}")
+    return torch.cuda.stream(stream)
+
+
 def _need_err(err, device):
     if _off(err, torch.int32, device):
         _refuse(err, torch.int32, "err", device)
@@ -483,8 +496,9 @@ def kv_read_q4(kq, vq, ksc, vsc, row_off, t0, k_out=None, v_out=None, n_rows=Non
     if k_out is None:
         if n_rows is None:
             raise ValueError("give k_out and v_out, or n_rows")
-        k_out = torch.zeros((int(n_rows), Hk, D), dtype=dtype, device=kq.device)
-        v_out = torch.zeros_like(k_out)
+        with _making(stream, device):
+            k_out = torch.zeros((int(n_rows), Hk, D), dtype=dtype, device=kq.device)
+            v_out = torch.zeros_like(k_out)
     elif not isinstance(k_out, torch.Tensor):
         raise TypeError("k_out must be a torch.Tensor")
     else:
@@ -508,7 +522,7 @@ def kv_read_q4(kq, vq, ksc, vsc, row_off, t0, k_out=None, v_out=None, n_rows=Non
 
 
 def _visible_args(q, kv_len, seq_of, n_seq, Hk, cap, Dk, max_kv_len, window, n_sink, out, ws, err,
-                  kind, device):
+                  kind, device, stream):
     """The arguments that the calls with a visible set share, checked: (T, H, max_kv_len, out, ws)."""
     if _off(q, torch.float32, device) or _off(kv_len, torch.int32, device):
         _refuse(q, torch.float32, "q", device)
@@ -525,7 +539,8 @@ def _visible_args(q, kv_len, seq_of, n_seq, Hk, cap, Dk, max_kv_len, window, n_s
     if not (0 <= window < 1 << 31 and 0 <= n_sink < 1 << 31 and max_kv_len < 1 << 31):
         raise ValueError("window, n_sink and max_kv_len must lie in [0, 2^31)")
     if out is None:
-        out = torch.empty_like(q)
+        with _making(stream, device):
+            out = torch.empty_like(q)
     else:
         if _off(out, torch.float32, device):
             _refuse(out, torch.float32, "out", device)
@@ -535,7 +550,8 @@ def _visible_args(q, kv_len, seq_of, n_seq, Hk, cap, Dk, max_kv_len, window, n_s
             raise ValueError("out must not be q")
     if ws is None:
         budget = min(window + n_sink, (1 << 31) - 1) if window else -1
-        ws = alloc_workspace(T, H, Hk, D, min(max_kv_len, cap), budget, kind, q.device, n_seq)
+        with _making(stream, device):
+            ws = alloc_workspace(T, H, Hk, D, min(max_kv_len, cap), budget, kind, q.device, n_seq)
     elif ws.get_device() != device or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous tensor on the current CUDA device")
     if err is not None:
@@ -564,7 +580,8 @@ def attn_decode_q4(q, kq, vq, ksc, vsc, kv_len, scale=None, k_scale=1.0, v_scale
     window = 0 if window is None else int(window)
     n_sink = int(n_sink) if window else 0
     T, H, max_kv_len, out, ws = _visible_args(q, kv_len, seq_of, n_seq, Hk, cap, D, max_kv_len,
-                                              window, n_sink, out, ws, err, KIND_Q4, device)
+                                              window, n_sink, out, ws, err, KIND_Q4, device,
+                                              stream)
     gs = 0 if gate is None else _visible_gate(gate, gate_stride, T, H, D, device)
     _check(LIB.attn_decode_q4(q.data_ptr(), kq.data_ptr(), vq.data_ptr(), ksc.data_ptr(),
                               vsc.data_ptr(), k_scale, v_scale, window, n_sink, out.data_ptr(),
@@ -592,7 +609,8 @@ def attn_decode_f16_window(q, k_cache, v_cache, kv_len, window, n_sink=0, scale=
     n_sink = int(n_sink)
     n_seq, cap, Hk, D = shape
     T, H, max_kv_len, out, ws = _visible_args(q, kv_len, seq_of, n_seq, Hk, cap, D, max_kv_len,
-                                              window, n_sink, out, ws, err, KIND_F16_WINDOW, device)
+                                              window, n_sink, out, ws, err, KIND_F16_WINDOW, device,
+                                              stream)
     gs = 0 if gate is None else _visible_gate(gate, gate_stride, T, H, D, device)
     _check(LIB.attn_decode_f16_window(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), window,
                                       n_sink, out.data_ptr(), kv_len.data_ptr(), _ptr(seq_of), T,

@@ -466,6 +466,34 @@ def test_other_stream_and_shared_workspace():
         assert_close(g.cpu().numpy(), ref, TOL, "side stream")
 
 
+def test_a_call_makes_its_tensors_on_its_own_stream():
+    """No output, no workspace given: the current stream is busy while the side stream's call runs, and
+    the memory held other bytes before."""
+    gd = _gd()
+    rng = np.random.default_rng(12)
+    side, D, lens = torch.cuda.Stream(), 128, [700, 0, 90]
+    cache = q4_cache(rng, lens, 2, 704, D)
+    q = rows(rng, 3, 8, D)
+    ref = oracle.decode_q4(q, *cache, lens, D ** -0.5)
+    args = [dev(q), *map(dev, cache), i32(lens)]
+    off, t0 = i32([0, 3, 3, 3]), i32([5, 0, 0])
+    with torch.cuda.stream(side):
+        poison = torch.full((4 << 20,), 255, dtype=torch.uint8, device="cuda")
+        poison2 = torch.full((64 << 10,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    del poison, poison2
+    with forced_chunk(128):
+        torch.cuda._sleep(20_000_000)
+        got = gd.attn_decode_q4(*args, stream=side)
+        k, _ = gd.kv_read_q4(*args[1:5], off, t0, n_rows=5, stream=side)
+    side.synchronize()
+    with torch.cuda.stream(side):
+        got, k = got.cpu().numpy(), k.cpu().numpy()
+    assert_close(got, ref, TOL, "side stream")
+    kd = oracle.dequant_q4(cache[0][0, :, 5:8], cache[2][0, :, 5:8]).transpose(1, 0, 2)
+    assert np.array_equal(k, np.concatenate([kd, np.zeros((2, 2, D))]).astype(np.float32))
+
+
 def test_offsets_past_32_bits():
     """A cache of more than 2^32 bytes of codes a side; only the last head's last positions and its
     first ones are seen."""
