@@ -75,7 +75,7 @@ __device__ __forceinline__ bool q4_place(const Q4Rows& a, const Q4Slot& sl, long
     flag_error(a.err, GQA_ERR_SEQ_RANGE);
     return false;
   }
-  const long long pos = (long long)__ldg(a.t0 + s) + (sl.r - first);
+  const long long pos = (long long)__ldg(a.t0 + s) + sl.r - first;
   if (pos < 0 || pos >= a.cap) {
     flag_error(a.err, GQA_ERR_KVLEN_RANGE);
     return false;
