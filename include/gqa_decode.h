@@ -88,12 +88,12 @@ typedef struct gqa_plan {
                         by sequence are merged inside the kernel by the group's chunk CTAs when
                         the grid fits one CTA per SM, else by a second kernel, one warp per
                         (row, head) */
-  int streamk;       /* 1: stream-K split (f16 caches): the (row, KV head, position) stream is
-                        cut into equal shares, one per CTA of a persistent grid */
+  int streamk;       /* 1: stream-K split (f16 and 4-bit caches): the (row, KV head, position)
+                        stream is cut into equal shares, one per CTA of a persistent grid */
   int row_group;     /* rows one CTA serves from a shared K/V tile: > 1 when rows may share a
                         sequence (n_seq < n_tok; f16 caches with head_dim 64 or 128 and group
-                        size 1, 2, 4 or 8, or TurboQuant caches with head_dim 64 or 128), else
-                        1 */
+                        size 1, 2, 4 or 8, TurboQuant caches with head_dim 64 or 128, 4-bit
+                        caches, and windowed f16 calls with head_dim 64 or 128), else 1 */
   size_t ws_bytes;   /* workspace the call needs (0 when merge == 0) */
 } gqa_plan;
 
@@ -109,8 +109,11 @@ typedef struct gqa_plan {
  * When rows may share a sequence (n_seq < n_tok) an f16 or TurboQuant call groups the rows of
  * each run of equal seq_of[] values (up to 64 / group size rows) into one CTA that reads each
  * K/V tile once for all of them; the chunks are then sized for the groups rather than the rows.
- * num_sms <= 0 queries the current CUDA device.  budget < 0 means dense (no id list).  n_seq
- * is the number of sequences in the cache, as passed to the decode call.
+ * num_sms <= 0 queries the current CUDA device.  budget < 0 means dense (no id list); with
+ * GQA_KIND_Q4 and GQA_KIND_F16_WINDOW it is window + n_sink (capped at INT32_MAX), or < 0 without a
+ * window.  Their splits: chunks of tiles of what a row sees, or, for long rows of a 4-bit cache,
+ * equal shares of all rows (streamk).  n_seq is the number of sequences in the cache, as passed to
+ * the decode call.
  * Returns GQA_EINVAL on bad sizes, GQA_EUNSUPPORTED for group sizes > 16.
  */
 gqa_status attn_decode_plan(int n_tok, int n_seq, int n_heads, int n_kv_heads, int head_dim,
