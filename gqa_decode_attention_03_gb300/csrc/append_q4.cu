@@ -6,8 +6,8 @@
 // a warp covers whole 32-byte sectors; two threads share the scale of 16 dims in appending.  New rows
 // are asked for before their place is known: their address does not depend on it.
 //
-// Bound by memory: 21600 rows of 8 heads of 128 dims appended and read back as fp32 in 63.0 us on
-// GB300, 405 MB at 6.4 TB/s; six sequences of up to 8192 rows read in 38.8 us, 228 MB at 5.9 TB/s.
+// Bound by memory: 19937 rows of 8 heads of 128 dims appended and read back as fp32 in 63.0 us on
+// GB300, 373 MB at 5.9 TB/s; six sequences of up to 8192 rows read in 38.8 us, 228 MB at 5.9 TB/s.
 // With the codes found by comparisons alone appending was bound by instructions (95 us in all).
 #include <cuda_runtime_api.h>
 
