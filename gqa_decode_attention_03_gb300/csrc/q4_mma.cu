@@ -2,13 +2,14 @@
 //
 // A CTA works on a piece of the list of tiles that a (group of rows, KV head x head split) sees: a
 // chunk of it, one a CTA, or, where that would take several waves of long chunks, an equal share of
-// all lists end to end (the 16-row ragged batch: 59.3 us against 69.8).  Each of its four warps
+// all lists end to end (the 16-row ragged batch: 57.2 us against 69.8).  Each of its four warps
 // (eight where a grid leaves no SM a second CTA) streams every fourth (eighth) tile of the piece
 // through a ring of its own and keeps its own running maximum, sum and accumulator, so nothing but
 // the end of the piece synchronises the CTA.  The pieces of a list meet in a cluster of their CTAs'
 // shared memories where one wave of clusters holds the grid, else through the workspace.  A tile
 // is TP positions of one KV head: four contiguous runs of the head-major cache (codes and scales of
-// K and of V), which the warp's first lane copies with cp.async.bulk; the ring holds NST tiles.
+// K and of V), which four lanes copy with cp.async.bulk, one each (the batch 58.0 us, 59.0 where one
+// lane copies all four); the ring holds NST tiles.
 //
 // A group is one row, or, where rows share sequences, the consecutive rows whose (row, head) pairs
 // fill the 8 rows of the products that a row's heads leave empty: their tiles are those of the
@@ -34,7 +35,7 @@
 //
 // Bound by instruction issue: 301 warp instructions per 16 positions and KV head (D = 128, 4 heads),
 // 64 conversions and 64 scale products among them, at 64 % of the issue slots; 57 rows of 16384
-// positions take 187 us, 5.76 TB/s, 86 % of the copy rate.
+// positions take 186 us, 5.8 TB/s, 87 % of the copy rate.
 #include <atomic>
 #include <type_traits>
 
@@ -62,7 +63,13 @@ struct Q4Cfg {
   static constexpr int MT = D / 16;                 // m-tiles of v.p
   static constexpr bool QSMEM = D == 256 && PN > 1;  // q's fragments stay in shared memory
   static constexpr int RING = NW * NST * STAGE;
-  static constexpr int MERGE = NW * NP * (D + 2) * 4;  // the warps' states, over the rings
+  // the warps' states, over the rings: rows of D values, maximum and sum, where a thread group's D / 8
+  // values are followed by two more words and rows lie 8 banks apart, so that the 16 pairs of values
+  // that a half warp stores at a time meet no bank twice (D = 256, eight warps: this merge 0.8 us
+  // against 1.5 with rows of D + 2)
+  static constexpr int MS = (D + 18 + 23) / 32 * 32 + 8;
+  __host__ __device__ static constexpr int mcol(int d) { return d + 2 * (d / (D / 8)); }
+  static constexpr int MERGE = NW * NP * MS * 4;
   // q's fragments: in a place of their own, or (then read into registers) in warp 0's last stage
   // before it takes its first tile
   static constexpr int QF_BYTES = PN * KS * 32 * 8;
@@ -131,9 +138,10 @@ __device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const
   const PartialParams& p = qp.base;
   __shared__ Q4Run s_runs[C::NW][9];
   __shared__ float s_amax[C::NW][C::NP];
-  const int kvh = it.y / p.head_split;
-  const int G = p.group / p.head_split;  // query heads of this CTA (<= 8)
-  const int head0 = kvh * p.group + (it.y % p.head_split) * G;
+  const int kvh = p.head_split == 1 ? it.y : it.y / p.head_split;
+  const int G = qp.heads;                // query heads of this CTA (<= 8)
+  auto row_of = [&](int pair) { return pair * qp.row_mul >> 8; };  // pair / G, pair <= 8
+  const int head0 = kvh * p.group + (it.y - kvh * p.head_split) * G;
   const int t0 = it.z * qp.rows, nr = min(qp.rows, p.n_tok - t0);
   const int np = nr * G;                 // pairs (<= 4 PN): row i / G, head i % G
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -145,7 +153,7 @@ __device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const
   float4 qx[PN][QW];
 #pragma unroll
   for (int pn = 0; pn < PN; ++pn) {
-    const int pair = 4 * pn + (gid >> 1), row = pair < np ? pair / G : 0;
+    const int pair = 4 * pn + (gid >> 1), row = pair < np ? row_of(pair) : 0;
     const bool on = pair < np && qon;
     const float* qrow =
         p.q + ((size_t)(t0 + row) * p.n_heads + head0 + (pair < np ? pair - row * G : 0)) * D;
@@ -167,7 +175,7 @@ __device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const
   int prow[PN], prun[PN];
 #pragma unroll
   for (int pn = 0; pn < PN; ++pn) {
-    prow[pn] = 4 * pn + tig < np ? (4 * pn + tig) / G : 0;
+    prow[pn] = 4 * pn + tig < np ? row_of(4 * pn + tig) : 0;
     prun[pn] = -1;
   }
   int nruns = 0, n = 0;
@@ -235,21 +243,20 @@ __device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const
   Q4Walk<C::TP> ahead, walk;
   ahead.start(runs);
   walk.start(runs);
-  auto issue = [&](int i, int st) {  // tile i's four runs of bytes into stage st (lane 0 copies)
+  // lanes 0 .. 3 copy a tile's codes and scales of K and of V: where from, bytes of a position, where to
+  const uint8_t* src = static_cast<const uint8_t*>(
+      lane == 0 ? p.kc : lane == 1 ? p.vc : lane == 2 ? (const void*)p.ksc : (const void*)p.vsc);
+  const int width = lane < 2 ? C::RB : C::SB;
+  const int at = lane < 2 ? lane * C::TP * C::RB : 2 * C::TP * C::RB + (lane - 2) * C::TP * C::SB;
+  auto issue = [&](int i, int st) {  // asks for tile i's positions, into stage st
     int start, end;
     ahead.tile(runs, i, start, end);
-    if (lane) return;
+    if (lane >= 4) return;
     const int m = min(C::TP, (end - start + 15) & ~15);  // cache_cap is a multiple of 16
     const size_t row = ((size_t)ahead.r.seq * p.n_kv_heads + kvh) * p.cache_cap + start;
-    uint8_t* dst = ring + st * C::STAGE;
-    mbar_arrive_expect_tx(&full[st], 2 * m * (C::RB + C::SB));
-    bulk_load(dst, static_cast<const uint8_t*>(p.kc) + row * C::RB, m * C::RB, &full[st]);
-    bulk_load(dst + C::TP * C::RB, static_cast<const uint8_t*>(p.vc) + row * C::RB, m * C::RB,
-              &full[st]);
-    dst += 2 * C::TP * C::RB;
-    bulk_load(dst, reinterpret_cast<const uint8_t*>(p.ksc) + row * C::SB, m * C::SB, &full[st]);
-    bulk_load(dst + C::TP * C::SB, reinterpret_cast<const uint8_t*>(p.vsc) + row * C::SB,
-              m * C::SB, &full[st]);
+    if (lane == 0) mbar_arrive_expect_tx(&full[st], 2 * m * (C::RB + C::SB));
+    __syncwarp(0xfu);  // the bytes are expected before any arrive
+    bulk_load(ring + st * C::STAGE + at, src + row * width, m * width, &full[st]);
   };
   int issued = 0;  // the warp's tiles asked for so far
   for (int i = i0; issued < C::NST0 && i < i1; i += C::NW, ++issued) issue(i, issued);
@@ -549,15 +556,15 @@ __device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const
 
   // ---- the warps' states meet in shared memory (over the rings, which are drained)
   __syncthreads();
-  float* mg = reinterpret_cast<float*>(smem);  // [warp][pair][D + 2]
+  float* mg = reinterpret_cast<float*>(smem);  // [warp][pair][MS]
 #pragma unroll
   for (int pn = 0; pn < PN; ++pn) {
-    float* mrow = mg + (warp * C::NP + 4 * pn + tig) * (D + 2);
+    float* mrow = mg + (warp * C::NP + 4 * pn + tig) * C::MS;
 #pragma unroll
     for (int i = 0; i < C::MT; ++i)
-      *reinterpret_cast<float2*>(mrow + gid * (D / 8) + 2 * i) =
+      *reinterpret_cast<float2*>(mrow + gid * (D / 8 + 2) + 2 * i) =
           make_float2(o[pn][i][0] + o[pn][i][1], o[pn][i][2] + o[pn][i][3]);
-    if (gid == 0) *reinterpret_cast<float2*>(mrow + D) = make_float2(m_run[pn], l_run[pn]);
+    if (gid == 0) *reinterpret_cast<float2*>(mrow + D + 16) = make_float2(m_run[pn], l_run[pn]);
   }
   __shared__ float s_w[C::NW][C::NP], s_m[C::NP], s_l[C::NP];  // warps' weights; maximum and sum
   __syncthreads();
@@ -565,13 +572,13 @@ __device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const
     const int h = threadIdx.x;
     float M = -INFINITY, Ls = 0.f;
 #pragma unroll
-    for (int w = 0; w < C::NW; ++w) M = fmaxf(M, mg[(w * C::NP + h) * (D + 2) + D]);
+    for (int w = 0; w < C::NW; ++w) M = fmaxf(M, mg[(w * C::NP + h) * C::MS + D + 16]);
 #pragma unroll
     for (int w = 0; w < C::NW; ++w) {
-      const float* r = mg + (w * C::NP + h) * (D + 2);
-      const float e = r[D] == -INFINITY ? 0.f : fast_exp2(r[D] - M);
+      const float* r = mg + (w * C::NP + h) * C::MS + D + 16;
+      const float e = r[0] == -INFINITY ? 0.f : fast_exp2(r[0] - M);
       s_w[w][h] = e * qp.v_scale;
-      Ls = fmaf(r[D + 1], e, Ls);
+      Ls = fmaf(r[1], e, Ls);
     }
     s_m[h] = M == -INFINITY ? -INFINITY : M * kLn2;  // natural-log units
     s_l[h] = Ls;
@@ -589,7 +596,7 @@ __device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const
                          : (size_t)t * p.n_split * rec + (size_t)head * (D + 2));
   };
   for (int h = warp; h < np; h += C::NW) {         // a warp a pair
-    const int row = h / G, t = t0 + row, head = head0 + h - row * G;
+    const int row = row_of(h), t = t0 + row, head = head0 + h - row * G;
     const float inv = s_l[h] > 0.f ? 1.f / s_l[h] : 0.f;
     float* dst = p.cluster > 1 ? reinterpret_cast<float*>(smem + C::CP_OFF) + h * (D + 2)
                  : split       ? record(h, t, head) + (it.piece ? it.piece * rec : rec0)
@@ -602,7 +609,7 @@ __device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const
       float2 a = make_float2(0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < C::NW; ++w) {
-        const float2 x = *reinterpret_cast<const float2*>(mg + (w * C::NP + h) * (D + 2) + d);
+        const float2 x = *reinterpret_cast<const float2*>(mg + (w * C::NP + h) * C::MS + C::mcol(d));
         a.x = fmaf(x.x, e[w], a.x);
         a.y = fmaf(x.y, e[w], a.y);
       }
@@ -645,7 +652,7 @@ __device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const
         Ls = fmaf(l[r], e, Ls);
       }
       const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
-      const int row = h / G, t = t0 + row, head = head0 + h - row * G;
+      const int row = row_of(h), t = t0 + row, head = head0 + h - row * G;
       *reinterpret_cast<float2*>(p.out + ((size_t)t * p.n_heads + head) * D + d) =
           make_float2(gated(p, t, head, d, y.x * inv), gated(p, t, head, d + 1, y.y * inv));
     }
@@ -667,30 +674,48 @@ __device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const
   __threadfence();
   constexpr int TPP = D / 2;  // threads of a pair, two dims each
   static_assert((32 * C::NW) % TPP == 0, "whole pairs a pass");
+  constexpr int PPP = 32 * C::NW / TPP;  // pairs of a pass
   const int d = 2 * (threadIdx.x % TPP);
-  if (pieces <= kQ4FewPieces) {  // every thread on its own: all loads of its dims in one round trip
-    for (int h = threadIdx.x / TPP; h < np; h += 32 * C::NW / TPP) {
-      const int row = h / G, t = t0 + row, head = head0 + h - row * G;
-      const float* src = record(h, t, head);
-      float2 ml[kQ4FewPieces], v[kQ4FewPieces];
+  constexpr int FEW = NW == 8 ? kQ4MaxCluster : kQ4FewPieces;
+  if (pieces <= FEW) {  // everything in one round trip
+    constexpr int Q = cmax(C::NP / PPP, 1);
+    float2 v[Q][FEW];
 #pragma unroll
-      for (int k = 0; k < kQ4FewPieces; ++k) {  // past the last piece: the last one again, no weight
-        const float* r = src + (min(k, pieces - 1) ? min(k, pieces - 1) * rec : rec0);
-        ml[k] = __ldcg(reinterpret_cast<const float2*>(r + D));
-        v[k] = __ldcg(reinterpret_cast<const float2*>(r + d));
+    for (int q = 0; q < Q; ++q) {
+      const int h = min((int)threadIdx.x / TPP + q * PPP, np - 1), row = row_of(h);
+      const float* r = record(h, t0 + row, head0 + h - row * G);
+#pragma unroll
+      for (int k = 0; k < FEW; ++k) {  // past the last piece: the last one again, no weight
+        const int kk = min(k, pieces - 1);
+        v[q][k] = __ldcg(reinterpret_cast<const float2*>(r + (kk ? kk * rec : rec0) + d));
       }
+    }
+    float2* ml = reinterpret_cast<float2*>(smem);  // [pair][FEW]
+    if (threadIdx.x < np * FEW) {
+      const int h = threadIdx.x / FEW, k = threadIdx.x % FEW, row = row_of(h);
+      const float* r = record(h, t0 + row, head0 + h - row * G) + (k ? k * rec : rec0) + D;
+      ml[threadIdx.x] =
+          k < pieces ? __ldcg(reinterpret_cast<const float2*>(r)) : make_float2(-INFINITY, 0.f);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int h = threadIdx.x / TPP + q * PPP;
+      if (h >= np) break;
       float M = -INFINITY, Ls = 0.f;
 #pragma unroll
-      for (int k = 0; k < kQ4FewPieces; ++k) M = fmaxf(M, ml[k].x);
+      for (int k = 0; k < FEW; ++k) M = fmaxf(M, ml[h * FEW + k].x);
       float2 a = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int k = 0; k < kQ4FewPieces; ++k) {
-        const float e = k >= pieces || ml[k].x == -INFINITY ? 0.f : __expf(ml[k].x - M);
-        Ls = fmaf(ml[k].y, e, Ls);
-        a.x = fmaf(v[k].x, e, a.x);
-        a.y = fmaf(v[k].y, e, a.y);
+      for (int k = 0; k < FEW; ++k) {
+        const float2 s = ml[h * FEW + k];
+        const float e = s.x == -INFINITY ? 0.f : __expf(s.x - M);
+        Ls = fmaf(s.y, e, Ls);
+        a.x = fmaf(v[q][k].x, e, a.x);
+        a.y = fmaf(v[q][k].y, e, a.y);
       }
       const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
+      const int row = row_of(h), t = t0 + row, head = head0 + h - row * G;
       *reinterpret_cast<float2*>(p.out + ((size_t)t * p.n_heads + head) * D + d) =
           make_float2(gated(p, t, head, d, a.x * inv), gated(p, t, head, d + 1, a.y * inv));
     }
@@ -698,7 +723,7 @@ __device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const
   }
   float* wt = reinterpret_cast<float*>(smem);  // [pair][pieces]
   for (int h = warp; h < np; h += C::NW) {
-    const int row = h / G;
+    const int row = row_of(h);
     const float* src = record(h, t0 + row, head0 + h - row * G);
     float M = -INFINITY, Ls = 0.f;
     for (int cc = lane; cc < pieces; cc += 32) {
@@ -719,7 +744,7 @@ __device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const
   }
   __syncthreads();
   for (int h = threadIdx.x / TPP; h < np; h += 32 * C::NW / TPP) {
-    const int row = h / G, t = t0 + row, head = head0 + h - row * G;
+    const int row = row_of(h), t = t0 + row, head = head0 + h - row * G;
     const float* src = record(h, t, head) + d;
     const float* e = wt + h * pieces;
     float2 a = make_float2(0.f, 0.f);

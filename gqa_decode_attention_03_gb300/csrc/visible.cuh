@@ -38,6 +38,8 @@ struct Q4Params {
   PartialParams base;
   int rows;      // rows of a group: their (row, head) pairs are at most 8
   int columns;   // KV heads x head split
+  int heads;     // query heads of a CTA: group / head split
+  int row_mul;   // 256 / heads + 1: pair / heads is pair * row_mul >> 8 for pairs up to 8
   int wide;      // eight warps a CTA, one CTA an SM
   int balanced;  // one wave of CTAs with equal shares (rows 1, n_tok <= kQ4BalancedRows)
   float k_scale, v_scale;
@@ -51,10 +53,13 @@ __host__ __device__ constexpr int q4_ctas_per_sm(int head_dim, int pn) {
 }
 constexpr int kQ4BalancedRows = 256, kQ4MinTiles = 8;
 // A list's start and end, in tiles, in the balanced split.  16 ragged rows of up to 32768 positions:
-// 64.1 us counting 0, 60.2 counting 6, 59.3 counting 12, 61.3 counting 18; 64 of up to 12000: 129,
-// 92.5, 92.2, 95.3.
-constexpr int kQ4ListCost = 12;
-constexpr int kQ4FewPieces = 8;  // pieces merged in one round trip
+// 58.5 us counting 6, 57.2 counting 9, 58.0 counting 12; 64 of up to 12000: 89.4, 89.4, 90.4; 16 of up
+// to 16384, 48 heads over 4, D = 256: 92.0, 87.0, 86.7.  Counting 0 cost 64.1 against 59.3 and 129
+// against 92.2 when 12 was taken first.
+constexpr int kQ4ListCost = 9;
+// Pieces that the last CTA merges in one round trip; kQ4MaxCluster where eight warps serve a list
+// (one row of 48 heads over 4, D = 256, 8191 positions in 16 pieces: 16.0 us against 16.7).
+constexpr int kQ4FewPieces = 8;
 constexpr int kQ4MaxSplit = 1024;  // chunks of a row at most
 constexpr int kQ4MaxCluster = 16;  // ... that merge in a cluster
 constexpr int kWinRowsTile = 128;  // ... of the kernel for rows that share a sequence

@@ -18,11 +18,11 @@ bool q4_scale_ok(float s);  // append_q4.cu
 // - A grid that would give every CTA slot kQ4LongShare tiles or more is cut into chunks of kQ4Chunk
 //   positions (64 rows of up to 4096: 52.5 with 1024, 51.7 with 2048), or, where lists are kQ4LongList
 //   positions or longer, into equal shares of all lists in one wave (16 ragged rows of up to 32768:
-//   69.8 chunked, 59.3; 64 of up to 8192 85.5, 76.1; 64 of up to 4096 51.2, 46.0; 200 of up to 1024
+//   69.8 chunked, 57.2; 64 of up to 8192 85.5, 76.1; 64 of up to 4096 51.2, 46.0; 200 of up to 1024
 //   40.9, 49.4).
 // - A smaller one that has an SM for every list runs one CTA of eight warps an SM, a list in as many
-//   chunks as there are SMs (one row of 48 heads over 4, 8191 positions: 16.7 against 18.2 with four
-//   warps; 32 rows of two sequences, window 2048: 13.5 against 17.7).
+//   chunks as there are SMs (one row of 48 heads over 4, 8191 positions: 14.9 against 18.4 with four
+//   warps; 32 rows of two sequences, window 2048: 13.1 against 17.5).
 constexpr int kQ4Chunk = 2048, kQ4LongShare = 32, kQ4LongList = 2048;
 // Windowed f16 rows: as many chunks as fill the CTA slots once, of at most kWinMaxChunk positions.
 constexpr int kWinCtasPerSm = 2;
@@ -244,6 +244,8 @@ static gqa_status visible_common(int kind, const float* q, const void* kc, const
   } else if (q4) {
     qp.rows = plan.row_group;
     qp.columns = n_kv_heads * p.head_split;
+    qp.heads = p.group / p.head_split;
+    qp.row_mul = 256 / qp.heads + 1;
     qp.balanced = plan.streamk;
     qp.wide = !plan.streamk && ctas <= sms;
     e = launch_q4(head_dim, qp, grid, stream);
