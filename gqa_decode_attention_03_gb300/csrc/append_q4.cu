@@ -6,11 +6,13 @@
 // a warp covers whole 32-byte sectors; two threads share the scale of 16 dims in appending.  New rows
 // are asked for before their place is known: their address does not depend on it.
 //
-// Bound by memory: 19937 rows of 8 heads of 128 dims appended and read back as fp32 in 63.0 us on
-// GB300, 373 MB at 5.9 TB/s; six sequences of up to 8192 rows read in 38.8 us, 228 MB at 5.9 TB/s.
-// With the codes found by comparisons alone appending was bound by instructions (95 us in all).
+// Bound by memory: 19937 rows of 8 heads of 128 dims appended and read back as fp32 in 60.1 us on
+// GB300, 373 MB at 6.2 TB/s; six sequences of up to 8192 rows read in 36.1 us, 228 MB at 6.3 TB/s.
+// With the codes found by comparisons alone appending was bound by instructions (95 us in all); with
+// every row's sequence searched for anew the two took 63.4 and 39.0.
 #include <cuda_runtime_api.h>
 
+#include <climits>
 #include <cmath>
 #include <cstdio>
 #include <type_traits>
@@ -55,32 +57,41 @@ __device__ __forceinline__ Q4Slot q4_slot(const Q4Rows& a, int j) {
   return s;
 }
 
+// The sequence found last: it holds rows [first, next) of the batch.
+struct Q4Seq {
+  int s = -1, first = 0, next = INT_MIN;
+};
+
 // The cache row of the thread's row; false when no sequence holds it or its position is none of the
-// cache's (flagged).  Every lane of the warp has to call it; a warp's rows are consecutive.
+// cache's (flagged).  Every lane of the warp has to call it; a warp's rows are consecutive, and the
+// search is made anew only where they leave the sequence that the ones before belong to.
 template <int D, int DPT>
-__device__ __forceinline__ bool q4_place(const Q4Rows& a, const Q4Slot& sl, long long& crow) {
+__device__ __forceinline__ bool q4_place(const Q4Rows& a, const Q4Slot& sl, Q4Seq& q, long long& crow) {
   constexpr int RPW = D / DPT >= 32 ? 1 : 32 / (D / DPT);  // rows of a warp
   const int end = min(__ldg(a.row_off + a.n_seq), a.n_rows);
   const int r_first = __shfl_sync(0xffffffffu, sl.r, 0);
-  int s = -1;
+  Q4Seq mine;
 #pragma unroll
   for (int k = 0; k < RPW; ++k) {
     if (r_first >= end - k) break;  // (r_first + k >= end, without overflow)
-    const int f = ragged_find(a.row_off, a.n_seq, r_first + k);
-    if (sl.r == r_first + k) s = f;
+    if (r_first + k >= q.next) {
+      q.s = ragged_find(a.row_off, a.n_seq, r_first + k);
+      q.first = __ldg(a.row_off + max(q.s, 0));
+      q.next = q.s < 0 ? INT_MIN : __ldg(a.row_off + q.s + 1);
+    }
+    if (sl.r == r_first + k) mine = q;
   }
   if (sl.r >= end) return false;
-  const int first = s < 0 ? 0 : __ldg(a.row_off + s);
-  if (s < 0 || sl.r < first || sl.r >= __ldg(a.row_off + s + 1)) {
+  if (mine.s < 0 || sl.r < mine.first || sl.r >= mine.next) {
     flag_error(a.err, GQA_ERR_SEQ_RANGE);
     return false;
   }
-  const long long pos = (long long)__ldg(a.t0 + s) + sl.r - first;
+  const long long pos = (long long)__ldg(a.t0 + mine.s) + sl.r - mine.first;
   if (pos < 0 || pos >= a.cap) {
     flag_error(a.err, GQA_ERR_KVLEN_RANGE);
     return false;
   }
-  crow = ((long long)s * a.hk + sl.head) * a.cap + pos;
+  crow = ((long long)mine.s * a.hk + sl.head) * a.cap + pos;
   return true;
 }
 
@@ -188,7 +199,8 @@ __global__ void __launch_bounds__(kQ4Threads<D, 8, kRowBlock>)
     v1 = __ldcs(reinterpret_cast<const float4*>(v_new + sl.elem) + 1);
   }
   long long crow = 0;
-  const bool on = q4_place<D, 8>(a, sl, crow);
+  Q4Seq seq;
+  const bool on = q4_place<D, 8>(a, sl, seq, crow);
   uint32_t kc, ks, vc, vs;
   q4_quantise(k0, k1, a.k_scale, kc, ks);
   q4_quantise(v0, v1, a.v_scale, vc, vs);
@@ -202,11 +214,15 @@ __global__ void __launch_bounds__(kQ4Threads<D, 8, kRowBlock>)
   }
 }
 
-// A thread's rows in reading: f16 8 dims of a row, fp32 4 dims of two rows 8 apart.
+// A thread in reading: f16 8 dims of one row or two 8 apart, fp32 4 dims of two rows 8 apart or four 4
+// apart.  More rows a thread read faster (24422 rows of 8 heads of 128: fp32 36.1 us against 36.8, f16
+// 23.8 against 26.0) but their sequences are looked up one after another (64 sequences of one row or
+// none, appended and read: 7.3 us against 5.6), so batches of kReadMany rows or more take them.
 template <typename T>
 constexpr int kReadDims = sizeof(T) == 4 ? 4 : 8;
-template <typename T>
-constexpr int kReadRows = sizeof(T) == 4 ? 8 : kRowBlock;
+template <typename T, bool MANY>
+constexpr int kReadRows = (sizeof(T) == 4 ? 8 : kRowBlock) / (MANY ? 2 : 1);
+constexpr int kReadMany = 2048;
 
 // The codes of a thread's dims, and their values times s, stored.
 template <typename T>
@@ -240,21 +256,22 @@ __device__ __forceinline__ void q4_store(T* dst, uint32_t codes, float s) {
   }
 }
 
-template <int D, typename T>
-__global__ void __launch_bounds__(kQ4Threads<D, kReadDims<T>, kReadRows<T>>)
+template <int D, typename T, bool MANY>
+__global__ void __launch_bounds__(kQ4Threads<D, kReadDims<T>, kReadRows<T, MANY>>)
     read_q4_kernel(T* __restrict__ k_out, T* __restrict__ v_out, Q4Rows a) {
-  constexpr int DPT = kReadDims<T>, N = kRowBlock / kReadRows<T>;
+  constexpr int DPT = kReadDims<T>, ROWS = kReadRows<T, MANY>, N = kRowBlock / ROWS;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   const int slice = threadIdx.x % (D / DPT);
   Q4Slot sl[N];
+  Q4Seq seq;
   bool on[N];
   uint32_t kc[N], vc[N], ks[N], vs[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    sl[j] = q4_slot<D, DPT>(a, j * kReadRows<T>);
+    sl[j] = q4_slot<D, DPT>(a, j * ROWS);
     long long crow = 0;
-    on[j] = q4_place<D, DPT>(a, sl[j], crow);
+    on[j] = q4_place<D, DPT>(a, sl[j], seq, crow);
     kc[j] = vc[j] = ks[j] = vs[j] = 0;
     if (on[j]) {
       kc[j] = q4_load<T>(a.kq + crow * (D / 2) + slice * (DPT / 2));
@@ -355,14 +372,19 @@ extern "C" gqa_status kv_read_q4(const uint8_t* kq, const uint8_t* vq, const uin
                 row_off, t0, err_word, n_rows, n_kv_heads, n_seq, cache_cap, k_scale, v_scale};
   return gqa::q4_rows_call("kv_read_q4", a, head_dim, k_out, v_out, [&](unsigned blocks) {
     using namespace gqa;
-    auto launch = [&](auto d) {
+    auto run = [&](auto d, auto* k, auto* v, auto many) {
       constexpr int D = decltype(d)::value;
-      return out_f16 ? q4_launch(read_q4_kernel<D, __half>, blocks,
-                                 kQ4Threads<D, kReadDims<__half>, kReadRows<__half>>, stream,
-                                 static_cast<__half*>(k_out), static_cast<__half*>(v_out), a)
-                     : q4_launch(read_q4_kernel<D, float>, blocks,
-                                 kQ4Threads<D, kReadDims<float>, kReadRows<float>>, stream,
-                                 static_cast<float*>(k_out), static_cast<float*>(v_out), a);
+      constexpr bool MANY = decltype(many)::value;
+      using T = std::remove_pointer_t<decltype(k)>;
+      return q4_launch(read_q4_kernel<D, T, MANY>, blocks,
+                       kQ4Threads<D, kReadDims<T>, kReadRows<T, MANY>>, stream, k, v, a);
+    };
+    auto launch = [&](auto d) {
+      auto out = [&](auto* k, auto* v) {
+        return a.n_rows >= kReadMany ? run(d, k, v, std::true_type()) : run(d, k, v, std::false_type());
+      };
+      return out_f16 ? out(static_cast<__half*>(k_out), static_cast<__half*>(v_out))
+                     : out(static_cast<float*>(k_out), static_cast<float*>(v_out));
     };
     if (head_dim == 64) return launch(std::integral_constant<int, 64>());
     if (head_dim == 128) return launch(std::integral_constant<int, 128>());

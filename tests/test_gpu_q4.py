@@ -72,6 +72,31 @@ def test_append_is_bit_exact(D, Hk, k_scale, v_scale):
     assert int(err) == 0
 
 
+@pytest.mark.parametrize("D,dtype", [(64, torch.float16), (128, torch.float32),
+                                     (128, torch.float16), (256, torch.float32),
+                                     (256, torch.float16)])
+def test_many_rows_of_ragged_sequences_read(D, dtype):
+    """More than 2048 rows, sequences that end anywhere in a block of 16 rows; rows behind the last one
+    keep what they held."""
+    rng = np.random.default_rng(D)
+    counts, Hk, cap, pad = [1003, 0, 1, 2, 0, 0, 17, 700, 400, 5], 3, 1008, 9
+    n, n_seq = sum(counts), len(counts)
+    t0 = [int(rng.integers(0, cap - c + 1)) for c in counts]
+    codes = rng.integers(0, 256, (2, n_seq, Hk, cap, D // 2), dtype=np.uint8)
+    scales = rng.integers(40, 88, (2, n_seq, Hk, cap, D // 16), dtype=np.uint8)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    k = torch.full((n + pad, Hk, D), 7.0, dtype=dtype, device="cuda")
+    v = k.clone()
+    _gd().kv_read_q4(dev(codes[0]), dev(codes[1]), dev(scales[0]), dev(scales[1]),
+                     i32(ragged(counts)), i32(t0), k_out=k, v_out=v, v_scale=2.0, err=err)
+    for got, side, scale in ((k, 0, 1.0), (v, 1, 2.0)):
+        plane = oracle.dequant_q4(codes[side], scales[side], scale).transpose(0, 2, 1, 3)
+        ref = np.concatenate([plane[s, t:t + c] for s, (c, t) in enumerate(zip(counts, t0))])
+        assert np.array_equal(got[:n].cpu().numpy(), torch.from_numpy(ref).to(dtype).numpy())
+        assert (got[n:] == 7.0).all()
+    assert int(err) == 0
+
+
 @pytest.mark.parametrize("n_seq", [1, 31, 32, 33, 1024, 1025, 5000])
 def test_rows_find_their_sequence(n_seq):
     """One KV head of 64 dims, many sequences of 0 to 3 rows: reading back what was appended."""
