@@ -1,15 +1,16 @@
 // append_q4.cu -- rows into and out of the 4-bit cache (kv_append_q4, kv_read_q4).
 //
-// A CTA takes 16 rows of one KV head, K and V: where they belong to one sequence, one run of the
-// head-major cache, so that its scales (8 bytes a position at D = 128) meet in whole 32-byte sectors.
-// A thread holds 8 consecutive dims of a row, 4 where it writes fp32, so that every load and store of
-// a warp covers whole 32-byte sectors; two threads share the scale of 16 dims in appending.  New rows
-// are asked for before their place is known: their address does not depend on it.
+// A row of a KV head is a unit; a CTA takes 16 units, K and V, in the batch's own order, so that the
+// fp32 side is one run of memory (reading six sequences of up to 8192 rows of 8 heads of 128, caches
+// and outputs not in L2: 38.0 us against 40.7 where a CTA takes 16 rows of one head).  A thread holds 8
+// consecutive dims of a unit, 4 where it writes fp32, so that every load and store of a warp covers
+// whole 32-byte sectors of rows and codes; two threads share the scale of 16 dims in appending.  New
+// rows are asked for before their place is known: their address does not depend on it.
 //
-// Bound by memory: 19937 rows of 8 heads of 128 dims appended and read back as fp32 in 60.1 us on
-// GB300, 373 MB at 6.2 TB/s; six sequences of up to 8192 rows read in 36.1 us, 228 MB at 6.3 TB/s.
-// With the codes found by comparisons alone appending was bound by instructions (95 us in all); with
-// every row's sequence searched for anew the two took 63.4 and 39.0.
+// Bound by memory: 19937 rows of 8 heads of 128 dims appended and read back as fp32 in 59.8 us on
+// GB300, 373 MB at 6.2 TB/s; the sequences above read at 6.0 TB/s, 228 MB.  With the codes found by
+// comparisons alone appending was bound by instructions (95 us in all); with every row's sequence
+// searched for anew the two took 63.4 and 39.0 from L2 as far as it reached.
 #include <cuda_runtime_api.h>
 
 #include <climits>
@@ -24,7 +25,7 @@ namespace gqa {
 
 void set_last_error(const char* msg);  // host.cu: the text gqa_last_error() returns
 
-constexpr int kRowBlock = 16;
+constexpr int kUnits = 16;  // of a CTA
 
 struct Q4Rows {
   uint8_t *kq, *vq, *ksc, *vsc;
@@ -36,24 +37,23 @@ struct Q4Rows {
   float k_scale, v_scale;  // append: their inverses
 };
 
-// Threads of a CTA with DPT dims of ROWS rows at a time.
-template <int D, int DPT, int ROWS>
-constexpr int kQ4Threads = ROWS * (D / DPT);
+// Threads of a CTA with DPT dims of UNITS units at a time.
+template <int D, int DPT, int UNITS>
+constexpr int kQ4Threads = UNITS * (D / DPT);
 
-// A row of the batch, the thread's first element there, its KV head.
+// A row of the batch, its KV head, the thread's first element there.
 struct Q4Slot {
   int r, head;
   long long elem;
 };
-// The thread's row of rows j, j + 1, .. j + ROWS - 1 of the CTA's block.
+// The thread's unit of units j, j + 1, .. of the CTA's.
 template <int D, int DPT>
 __device__ __forceinline__ Q4Slot q4_slot(const Q4Rows& a, int j) {
-  const unsigned rb = blockIdx.x / static_cast<unsigned>(a.hk);
+  const unsigned u = blockIdx.x * kUnits + j + threadIdx.x / (D / DPT);
   Q4Slot s;
-  s.head = static_cast<int>(blockIdx.x - rb * a.hk);
-  const long long r = (long long)rb * kRowBlock + j + threadIdx.x / (D / DPT);
-  s.r = static_cast<int>(r < INT32_MAX ? r : INT32_MAX);
-  s.elem = (r * a.hk + s.head) * D + threadIdx.x % (D / DPT) * DPT;
+  s.r = static_cast<int>(u / a.hk);
+  s.head = static_cast<int>(u - s.r * a.hk);
+  s.elem = (long long)u * D + threadIdx.x % (D / DPT) * DPT;
   return s;
 }
 
@@ -63,11 +63,11 @@ struct Q4Seq {
 };
 
 // The cache row of the thread's row; false when no sequence holds it or its position is none of the
-// cache's (flagged).  Every lane of the warp has to call it; a warp's rows are consecutive, and the
-// search is made anew only where they leave the sequence that the ones before belong to.
+// cache's (flagged).  Every lane of the warp has to call it; a warp's units are consecutive, and the
+// search is made anew only where their rows leave the sequence that the ones before belong to.
 template <int D, int DPT>
 __device__ __forceinline__ bool q4_place(const Q4Rows& a, const Q4Slot& sl, Q4Seq& q, long long& crow) {
-  constexpr int RPW = D / DPT >= 32 ? 1 : 32 / (D / DPT);  // rows of a warp
+  constexpr int RPW = D / DPT >= 32 ? 1 : 32 / (D / DPT);  // units, and rows at most, of a warp
   const int end = min(__ldg(a.row_off + a.n_seq), a.n_rows);
   const int r_first = __shfl_sync(0xffffffffu, sl.r, 0);
   Q4Seq mine;
@@ -186,7 +186,7 @@ __device__ __forceinline__ void q4_quantise(const float4& x0, const float4& x1, 
 }
 
 template <int D>
-__global__ void __launch_bounds__(kQ4Threads<D, 8, kRowBlock>)
+__global__ void __launch_bounds__(kQ4Threads<D, 8, kUnits>)
     append_q4_kernel(const float* __restrict__ k_new, const float* __restrict__ v_new, Q4Rows a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
@@ -214,15 +214,11 @@ __global__ void __launch_bounds__(kQ4Threads<D, 8, kRowBlock>)
   }
 }
 
-// A thread in reading: f16 8 dims of one row or two 8 apart, fp32 4 dims of two rows 8 apart or four 4
-// apart.  More rows a thread read faster (24422 rows of 8 heads of 128: fp32 36.1 us against 36.8, f16
-// 23.8 against 26.0) but their sequences are looked up one after another (64 sequences of one row or
-// none, appended and read: 7.3 us against 5.6), so batches of kReadMany rows or more take them.
+// A thread in reading: 8 dims (fp32: 4) of two units 8 apart (f16: 25.3 us against 27.8 for the
+// sequences above with one; four of fp32 looked up 64 short sequences too slowly, 7.3 us against 5.6).
 template <typename T>
 constexpr int kReadDims = sizeof(T) == 4 ? 4 : 8;
-template <typename T, bool MANY>
-constexpr int kReadRows = (sizeof(T) == 4 ? 8 : kRowBlock) / (MANY ? 2 : 1);
-constexpr int kReadMany = 2048;
+constexpr int kReadUnits = 8;
 
 // The codes of a thread's dims, and their values times s, stored.
 template <typename T>
@@ -256,10 +252,10 @@ __device__ __forceinline__ void q4_store(T* dst, uint32_t codes, float s) {
   }
 }
 
-template <int D, typename T, bool MANY>
-__global__ void __launch_bounds__(kQ4Threads<D, kReadDims<T>, kReadRows<T, MANY>>)
+template <int D, typename T>
+__global__ void __launch_bounds__(kQ4Threads<D, kReadDims<T>, kReadUnits>)
     read_q4_kernel(T* __restrict__ k_out, T* __restrict__ v_out, Q4Rows a) {
-  constexpr int DPT = kReadDims<T>, ROWS = kReadRows<T, MANY>, N = kRowBlock / ROWS;
+  constexpr int DPT = kReadDims<T>, N = kUnits / kReadUnits;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   const int slice = threadIdx.x % (D / DPT);
@@ -269,7 +265,7 @@ __global__ void __launch_bounds__(kQ4Threads<D, kReadDims<T>, kReadRows<T, MANY>
   uint32_t kc[N], vc[N], ks[N], vs[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    sl[j] = q4_slot<D, DPT>(a, j * ROWS);
+    sl[j] = q4_slot<D, DPT>(a, j * kReadUnits);
     long long crow = 0;
     on[j] = q4_place<D, DPT>(a, sl[j], seq, crow);
     kc[j] = vc[j] = ks[j] = vs[j] = 0;
@@ -318,8 +314,10 @@ gqa_status q4_rows_call(const char* name, const Q4Rows& a, int head_dim, const v
     return bad(GQA_EINVAL, "the rows, codes and scales must be 16-byte aligned");
   if ((bits(a.row_off) | bits(a.t0) | bits(a.err)) & 3)
     return bad(GQA_EINVAL, "row_off, t0 and err_word must be 4-byte aligned");
-  const long long blocks = (a.n_rows + (long long)kRowBlock - 1) / kRowBlock * a.hk;
-  if (blocks > 0x7fffffffLL) return bad(GQA_EUNSUPPORTED, "too many rows for one launch");
+  const long long units = (long long)a.n_rows * a.hk;
+  if (units > INT32_MAX - kUnits)
+    return bad(GQA_EUNSUPPORTED, "n_rows * n_kv_heads must stay below 2^31 - 16");
+  const long long blocks = (units + kUnits - 1) / kUnits;
   const cudaError_t e = go(static_cast<unsigned>(blocks));
   if (e == cudaSuccess) return GQA_OK;
   (void)cudaGetLastError();
@@ -354,10 +352,10 @@ extern "C" gqa_status kv_append_q4(const float* k_new, const float* v_new, int n
     b.v_scale = 1.f / v_scale;
     using namespace gqa;
     if (head_dim == 64)
-      return q4_launch(append_q4_kernel<64>, blocks, kQ4Threads<64, 8, kRowBlock>, stream, k_new, v_new, b);
+      return q4_launch(append_q4_kernel<64>, blocks, kQ4Threads<64, 8, kUnits>, stream, k_new, v_new, b);
     if (head_dim == 128)
-      return q4_launch(append_q4_kernel<128>, blocks, kQ4Threads<128, 8, kRowBlock>, stream, k_new, v_new, b);
-    return q4_launch(append_q4_kernel<256>, blocks, kQ4Threads<256, 8, kRowBlock>, stream, k_new, v_new, b);
+      return q4_launch(append_q4_kernel<128>, blocks, kQ4Threads<128, 8, kUnits>, stream, k_new, v_new, b);
+    return q4_launch(append_q4_kernel<256>, blocks, kQ4Threads<256, 8, kUnits>, stream, k_new, v_new, b);
   });
 }
 
@@ -372,19 +370,14 @@ extern "C" gqa_status kv_read_q4(const uint8_t* kq, const uint8_t* vq, const uin
                 row_off, t0, err_word, n_rows, n_kv_heads, n_seq, cache_cap, k_scale, v_scale};
   return gqa::q4_rows_call("kv_read_q4", a, head_dim, k_out, v_out, [&](unsigned blocks) {
     using namespace gqa;
-    auto run = [&](auto d, auto* k, auto* v, auto many) {
-      constexpr int D = decltype(d)::value;
-      constexpr bool MANY = decltype(many)::value;
-      using T = std::remove_pointer_t<decltype(k)>;
-      return q4_launch(read_q4_kernel<D, T, MANY>, blocks,
-                       kQ4Threads<D, kReadDims<T>, kReadRows<T, MANY>>, stream, k, v, a);
-    };
     auto launch = [&](auto d) {
-      auto out = [&](auto* k, auto* v) {
-        return a.n_rows >= kReadMany ? run(d, k, v, std::true_type()) : run(d, k, v, std::false_type());
-      };
-      return out_f16 ? out(static_cast<__half*>(k_out), static_cast<__half*>(v_out))
-                     : out(static_cast<float*>(k_out), static_cast<float*>(v_out));
+      constexpr int D = decltype(d)::value;
+      return out_f16 ? q4_launch(read_q4_kernel<D, __half>, blocks,
+                                 kQ4Threads<D, kReadDims<__half>, kReadUnits>, stream,
+                                 static_cast<__half*>(k_out), static_cast<__half*>(v_out), a)
+                     : q4_launch(read_q4_kernel<D, float>, blocks,
+                                 kQ4Threads<D, kReadDims<float>, kReadUnits>, stream,
+                                 static_cast<float*>(k_out), static_cast<float*>(v_out), a);
     };
     if (head_dim == 64) return launch(std::integral_constant<int, 64>());
     if (head_dim == 128) return launch(std::integral_constant<int, 128>());

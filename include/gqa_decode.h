@@ -388,6 +388,7 @@ gqa_status attn_decode_tq_gated(const float* q_rot, const float* q_jl, const uin
  * sequence s with row_off[s] <= r < row_off[s + 1] and stands for position t0[s] + r - row_off[s].
  *   row_off       device int32 [n_seq + 1], ascending from 0; row_off[n_seq] <= n_rows.  A sequence
  *                 may have no rows; rows from row_off[n_seq] on (a padded batch) are left alone.
+ *   n_rows        rows of the batch; n_rows * n_kv_heads below 2^31 - 16 (GQA_EUNSUPPORTED).
  *   t0            device int32 [n_seq]
  * No two rows name the same position.  A row whose position falls outside [0, cache_cap) is
  * skipped and flagged GQA_ERR_KVLEN_RANGE; a row that no sequence holds, in a row_off that does

@@ -134,6 +134,12 @@ def test_read_refuses(gd, kw):
     assert read(gd, **kw) == gd.GQA_EINVAL and b"kv_read_q4" in gd.LIB.gqa_last_error()
 
 
+def test_rows_of_too_many_heads(gd):
+    for call in (append, read):
+        assert call(gd, n=1 << 27, hk=16) == gd.GQA_EUNSUPPORTED
+        assert b"n_rows * n_kv_heads" in gd.LIB.gqa_last_error()
+
+
 def test_no_rows_is_no_work(gd):
     assert append(gd, n=0, k_new=None) == gd.GQA_OK and read(gd, n=0, k_out=None) == gd.GQA_OK
 
