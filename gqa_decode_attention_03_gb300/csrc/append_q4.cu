@@ -70,10 +70,11 @@ __device__ __forceinline__ bool q4_place(const Q4Rows& a, const Q4Slot& sl, Q4Se
   constexpr int RPW = D / DPT >= 32 ? 1 : 32 / (D / DPT);  // units, and rows at most, of a warp
   const int end = min(__ldg(a.row_off + a.n_seq), a.n_rows);
   const int r_first = __shfl_sync(0xffffffffu, sl.r, 0);
+  const int r_last = __shfl_sync(0xffffffffu, sl.r, 31);  // (no row ahead: q serves the next units too)
   Q4Seq mine;
 #pragma unroll
   for (int k = 0; k < RPW; ++k) {
-    if (r_first >= end - k) break;  // (r_first + k >= end, without overflow)
+    if (r_first + k > r_last || r_first + k >= end) break;
     if (r_first + k >= q.next) {
       q.s = ragged_find(a.row_off, a.n_seq, r_first + k);
       q.first = __ldg(a.row_off + max(q.s, 0));
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(kQ4Threads<D, 8, kUnits>)
   }
 }
 
-// A thread in reading: 8 dims (fp32: 4) of two units 8 apart (f16: 25.3 us against 27.8 for the
+// A thread in reading: 8 dims (fp32: 4) of two units 8 apart (f16: 25.0 us against 27.8 for the
 // sequences above with one; four of fp32 looked up 64 short sequences too slowly, 7.3 us against 5.6).
 template <typename T>
 constexpr int kReadDims = sizeof(T) == 4 ? 4 : 8;

@@ -33,7 +33,7 @@
 //        interleaved nibble by nibble before the conversion.
 // Rows of 32 or 64 bytes are read without bank conflicts in k.q and two at a time at most in v.p.
 //
-// Bound by instruction issue: 301 warp instructions per 16 positions and KV head (D = 128, 4 heads),
+// Bound by instruction issue: 297 warp instructions per 16 positions and KV head (D = 128, 4 heads),
 // 64 conversions and 64 scale products among them, at 64 % of the issue slots; 57 rows of 16384
 // positions take 186 us, 5.8 TB/s, 87 % of the copy rate.
 #include <atomic>

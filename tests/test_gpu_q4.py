@@ -74,12 +74,13 @@ def test_append_is_bit_exact(D, Hk, k_scale, v_scale):
 
 @pytest.mark.parametrize("D,dtype", [(64, torch.float16), (128, torch.float32),
                                      (128, torch.float16), (256, torch.float32),
-                                     (256, torch.float16)])
-def test_many_rows_of_ragged_sequences_read(D, dtype):
+                                     (256, torch.float16), (64, torch.float32)])
+@pytest.mark.parametrize("Hk", [1, 3, 16])
+def test_many_rows_of_ragged_sequences_read(D, dtype, Hk):
     """More than 2048 rows, sequences that end anywhere in a block of 16 rows; rows behind the last one
     keep what they held."""
     rng = np.random.default_rng(D)
-    counts, Hk, cap, pad = [1003, 0, 1, 2, 0, 0, 17, 700, 400, 5], 3, 1008, 9
+    counts, cap, pad = [1003, 0, 1, 2, 0, 0, 17, 700, 400, 5, 1, 1, 0, 1, 1, 1], 1008, 9
     n, n_seq = sum(counts), len(counts)
     t0 = [int(rng.integers(0, cap - c + 1)) for c in counts]
     codes = rng.integers(0, 256, (2, n_seq, Hk, cap, D // 2), dtype=np.uint8)
@@ -195,6 +196,20 @@ def test_decode_window(D, window, n_sink, chunk):
         got = run_q4(q, cache, LENS, window=window, n_sink=n_sink).cpu().numpy()
     ref = oracle.decode_q4(q, *cache, LENS, D ** -0.5, window=window, n_sink=n_sink)
     assert_close(got, ref, TOL, f"window {window} sinks {n_sink} D {D}")
+
+
+@pytest.mark.parametrize("H,Hk,T", [(12, 1, 1), (48, 4, 1), (16, 4, 2), (32, 4, 2)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("L", [1300, 2040])
+def test_decode_lists_of_many_pieces(H, Hk, T, D, L):
+    """Lists of 9 to 16 pieces of eight warps: few lists merge in clusters, eight by the last CTA."""
+    rng = np.random.default_rng(H + D + L)
+    lens = [L] * T
+    cache = q4_cache(rng, lens, Hk, 2048, D)
+    q = rows(rng, T, H, D)
+    with forced_chunk(128):
+        got = _gd().attn_decode_q4(dev(q), *map(dev, cache), i32(lens))
+    assert_close(got.cpu().numpy(), oracle.decode_q4(q, *cache, lens, D ** -0.5), TOL, "pieces")
 
 
 @pytest.mark.parametrize("ctas", [1, 3, 7, 40, 500])
