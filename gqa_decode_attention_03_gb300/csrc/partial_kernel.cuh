@@ -233,12 +233,24 @@ __device__ __forceinline__ float warp_sum(float v) {
 // on the last ticket, so every call leaves it at zero.  Nobody waits for anybody: the CTAs that
 // are not last simply finish.  One warp per head; lane c holds chunk c's (m, l) and weight and
 // broadcasts the weight by shuffle, so a head's loads go out in one round.
+// ANY: on a counter that may hold whatever a call of another shape left there (last_of).
 struct NoEpilogue {  // merge_if_last writes the merged rows as they are
   template <int N>
   __device__ __forceinline__ void operator()(float (&)[N], int /*head*/, int /*lane*/) const {}
 };
 
-template <int D, class Epi = NoEpilogue>
+// Takes a ticket of n on a counter and tells whether it was the last; the counter is 0 again then.  What
+// it holds before the first may be anything that calls leave in a workspace: lengths, counts, and fp32
+// results, whose bits lie below those of this NaN, which no instruction makes (theirs is 0x7fffffff).
+constexpr unsigned kTicketBase = 0xffa50000u;
+__device__ __forceinline__ bool last_of(unsigned* counter, unsigned n) {
+  atomicMax(counter, kTicketBase);
+  const bool last = atomicAdd(counter, 1u) == kTicketBase + n - 1;
+  if (last) atomicExch(counter, 0u);
+  return last;
+}
+
+template <int D, bool ANY = false, class Epi = NoEpilogue>
 __device__ __forceinline__ void merge_if_last(const PartialParams& p, int t, int head0,
                                               int nheads, size_t counter, int nv, int ncw,
                                               const Epi& epi = Epi()) {
@@ -246,7 +258,8 @@ __device__ __forceinline__ void merge_if_last(const PartialParams& p, int t, int
   __threadfence();  // this thread's partial stores, visible device-wide before the ticket
   named_bar_sync(1, ncw * 32);
   if (threadIdx.x == 0)
-    s_last = atomicInc(p.counters + counter, (unsigned)(nv - 1)) == (unsigned)(nv - 1);
+    s_last = ANY ? last_of(p.counters + counter, nv)
+                 : atomicInc(p.counters + counter, (unsigned)(nv - 1)) == (unsigned)(nv - 1);
   named_bar_sync(1, ncw * 32);
   if (!s_last) return;
   __threadfence();

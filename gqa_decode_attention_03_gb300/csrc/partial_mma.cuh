@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(MmaCfg<D, NHG>::MAX_THREADS, MmaCfg<D, NHG>::M
     return;
   }
   if (p.merge)
-    merge_if_last<D>(p, t, g * G, G, (size_t)t * p.n_kv_heads + g, nchunks,
+    merge_if_last<D, WIN>(p, t, g * G, G, (size_t)t * p.n_kv_heads + g, nchunks,
                      C::NCW);
 }
 

@@ -666,8 +666,7 @@ __device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const
   __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();  // the CTA's records (ordered before by the barrier), then the ticket
-    s_last = atomicInc(p.counters + (size_t)it.z * qp.columns + it.y, (unsigned)(pieces - 1)) ==
-             (unsigned)(pieces - 1);
+    s_last = last_of(p.counters + (size_t)it.z * qp.columns + it.y, pieces);
   }
   __syncthreads();
   if (!s_last) return;

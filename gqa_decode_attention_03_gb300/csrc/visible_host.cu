@@ -48,6 +48,13 @@ static bool rows_grouped(bool q4, int n_tok, int n_seq, int n_heads, int group, 
          (!q4 || (long long)n_tok * n_heads * n >= kQ4RowsMinWork);
 }
 
+// Bytes of a workspace ahead of the partials: the arrival counters, a word per (row, head) so that
+// whatever a call's head split is, the counters of other calls over as many rows and heads lie there
+// too, dense f16 ones among them, which count on finding zeros.
+static size_t counter_bytes(int n_tok, int n_heads) {
+  return ((size_t)n_tok * n_heads * sizeof(uint32_t) + 255) / 256 * 256;
+}
+
 gqa_status plan_visible(int n_tok, int n_seq, int n_heads, int n_kv_heads, int head_dim,
                         int max_kv_len, int budget, int kind, int num_sms, gqa_plan* plan) {
   if (budget == 0 || budget < -1)
@@ -77,7 +84,8 @@ gqa_status plan_visible(int n_tok, int n_seq, int n_heads, int n_kv_heads, int h
     plan->merge = n_split > 1 ? 1 : 0;
     if (plan->merge) {
       const size_t part = (size_t)n_tok * n_split * n_heads * (head_dim + 2) * sizeof(float);
-      plan->ws_bytes = (part + 255) / 256 * 256 + (size_t)n_tok * sizeof(int32_t);
+      plan->ws_bytes = counter_bytes(n_tok, n_heads) + (part + 255) / 256 * 256 +
+                       (size_t)n_tok * sizeof(int32_t);
     }
     return GQA_OK;
   }
@@ -126,8 +134,8 @@ gqa_status plan_visible(int n_tok, int n_seq, int n_heads, int n_kv_heads, int h
     plan->grid_y = plan->grid_z = 1;
     plan->tile = tile;
     plan->merge = plan->streamk = 1;
-    const size_t cnt = ((size_t)n_tok * n_kv_heads * hs * sizeof(uint32_t) + 255) / 256 * 256;
-    plan->ws_bytes = cnt + 2 * (size_t)ctas * (group / hs) * (head_dim + 2) * sizeof(float);
+    plan->ws_bytes = counter_bytes(n_tok, n_heads) +
+                     2 * (size_t)ctas * (group / hs) * (head_dim + 2) * sizeof(float);
     return GQA_OK;
   }
   plan->chunk = (int)std::min<long long>(chunk * tile, INT_MAX / tile * tile);
@@ -139,8 +147,8 @@ gqa_status plan_visible(int n_tok, int n_seq, int n_heads, int n_kv_heads, int h
   plan->row_group = rows;
   plan->merge = n_split > 1 ? 1 : 0;
   if (plan->merge) {
-    const size_t cnt = ((size_t)n_tok * plan->grid_y * sizeof(uint32_t) + 255) / 256 * 256;
-    plan->ws_bytes = cnt + (size_t)n_tok * n_split * n_heads * (head_dim + 2) * sizeof(float);
+    plan->ws_bytes = counter_bytes(n_tok, n_heads) +
+                     (size_t)n_tok * n_split * n_heads * (head_dim + 2) * sizeof(float);
   }
   return GQA_OK;
 }
@@ -217,15 +225,12 @@ static gqa_status visible_common(int kind, const float* q, const void* kc, const
     while (p.group % p.head_split || p.group / p.head_split > 8) ++p.head_split;
   const bool grouped = rows_grouped(q4, n_tok, n_seq, n_heads, p.group, head_dim,
                                     budget > 0 ? std::min(max_len, budget) : max_len);
-  if (plan.merge && grouped) {  // ws = [partials][n_valid]
-    const size_t part = (size_t)n_tok * plan.n_split * n_heads * (head_dim + 2) * sizeof(float);
-    p.part = static_cast<float*>(ws);
-    p.n_valid = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + (part + 255) / 256 * 256);
-  } else if (plan.merge) {  // ws = [arrival counters][partials]
-    const size_t cnt =
-        ((size_t)n_tok * n_kv_heads * p.head_split * sizeof(uint32_t) + 255) / 256 * 256;
+  if (plan.merge) {  // ws = [arrival counters][partials], then [n_valid] where rows are grouped
+    char* part = static_cast<char*>(ws) + counter_bytes(n_tok, n_heads);
+    const size_t bytes = (size_t)n_tok * plan.n_split * n_heads * (head_dim + 2) * sizeof(float);
     p.counters = static_cast<unsigned int*>(ws);
-    p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + cnt);
+    p.part = reinterpret_cast<float*>(part);
+    if (grouped) p.n_valid = reinterpret_cast<int32_t*>(part + (bytes + 255) / 256 * 256);
   }
   p.gate = gate;
   p.gate_stride = gate ? gate_stride : 0;

@@ -428,7 +428,10 @@ gqa_status kv_read_q4(const uint8_t* kq, const uint8_t* vq, const uint8_t* ksc,
  *   window        >= 0; n_sink >= 0 (not used with window 0)
  *   gate          sigmoid output gate as in the _gated calls above, or NULL
  *   ws, ws_bytes  attn_decode_workspace_bytes(..., budget, GQA_KIND_Q4) with budget =
- *                 window + n_sink, or -1 without a window; zeroed once like attn_decode_f16's
+ *                 window + n_sink, or -1 without a window; as attn_decode_f16's, zeroed once.
+ *                 Its first n_tok * n_heads * 4 bytes (rounded up to 256) are counters,
+ *                 zero again after every call.  This call also finds its way where calls of
+ *                 other shapes have left partials there.
  *   other arguments and errors as attn_decode_f16
  */
 gqa_status attn_decode_q4(const float* q, const uint8_t* kq, const uint8_t* vq,
@@ -443,8 +446,8 @@ gqa_status attn_decode_q4(const float* q, const uint8_t* kq, const uint8_t* vq,
  * attn_decode_f16_window -- attn_decode_f16 through a window with sinks.
  *   window        >= 1; n_sink >= 0
  *   gate          sigmoid output gate as in the _gated calls above, or NULL
- *   ws, ws_bytes  attn_decode_workspace_bytes(..., window + n_sink, GQA_KIND_F16_WINDOW); zeroed
- *                 once like attn_decode_f16's
+ *   ws, ws_bytes  attn_decode_workspace_bytes(..., window + n_sink, GQA_KIND_F16_WINDOW); as
+ *                 attn_decode_q4's
  *   other arguments and errors as attn_decode_f16
  */
 gqa_status attn_decode_f16_window(const float* q, const uint16_t* k_cache,

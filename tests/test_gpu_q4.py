@@ -506,6 +506,64 @@ def test_other_stream_and_shared_workspace():
         assert_close(g.cpu().numpy(), ref, TOL, "side stream")
 
 
+def test_calls_of_every_kind_share_a_workspace():
+    """Dense and windowed f16 layers, 4-bit ones, rows of one sequence, more rows and fewer: one after
+    another on one workspace, each over what the ones before have left there."""
+    gd = _gd()
+    rng = np.random.default_rng(14)
+    Hk, H, D, cap, T = 2, 8, 128, 1200, 48
+    lens = [int(n) for n in rng.integers(0, cap + 1, T)]
+    lens[:3] = [cap, 0, 1100]
+    kv = [(rows(rng, T, cap, Hk, D)).astype(np.float16) for _ in range(2)]
+    cache = q4_cache(rng, lens, Hk, cap, D)
+    q = rows(rng, T, H, D)
+    qd, kd, vd, cd = dev(q), dev(kv[0]), dev(kv[1]), list(map(dev, cache))
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
+    scale = D ** -0.5
+
+    def dense(n):
+        out = gd.attn_decode_f16(qd[:n], kd, vd, i32(lens[:n]), ws=ws)
+        return out, oracle.decode_f16(q[:n], *kv, lens[:n], scale)
+
+    def window(n):
+        out = gd.attn_decode_f16_window(qd[:n], kd, vd, i32(lens[:n]), 700, 4, ws=ws)
+        return out, oracle.decode_f16_window(q[:n], *kv, lens[:n], scale, 700, 4)
+
+    def shared(n):
+        seq, ln = [0] * n, list(range(cap - n + 1, cap + 1))
+        with _env(GQA_F16_ROWS="on"):
+            out = gd.attn_decode_f16_window(qd[:n], kd[:1], vd[:1], i32(ln), 700, 4, seq_of=i32(seq),
+                                            ws=ws)
+        return out, oracle.decode_f16_window(q[:n], *kv, ln, scale, 700, 4, seq_of=seq)
+
+    def q4(n):
+        out = gd.attn_decode_q4(qd[:n], *cd, i32(lens[:n]), ws=ws)
+        return out, oracle.decode_q4(q[:n], *cache, lens[:n], scale)
+
+    def q4_shares(n):
+        with forced_ctas(40):
+            return q4(n)
+
+    def q4_shared(n):
+        seq, ln = [0] * n, list(range(lens[2] - n + 1, lens[2] + 1))
+        one = [x[2:3] for x in cd]
+        with _env(GQA_Q4_ROWS="on"):
+            out = gd.attn_decode_q4(qd[:n], *one, i32(ln), seq_of=i32(seq), ws=ws)
+        return out, oracle.decode_q4(q[:n], *[x[2:3] for x in cache], ln, scale, seq_of=seq)
+
+    # (a dense call counts on zeros where its counters lie, which partials of a call of fewer rows reach)
+    want = [(f, n) for f in (dense, window, q4, shared, q4_shared) for n in (6, T)]
+    want = [w for w in want if w != (dense, T)] + [(q4, 6), (dense, 6), (window, T), (q4, T)]
+    order = [want[i % len(want)] for i in rng.permutation(2 * len(want))]
+    for step, (f, n) in enumerate(order):
+        with forced_chunk(128):
+            got, ref = f(n)
+        assert_close(got.cpu().numpy(), ref, TOL, f"step {step}: {f.__name__} of {n} rows")
+        if step % 3 == 0:
+            got, ref = q4_shares(n)
+            assert_close(got.cpu().numpy(), ref, TOL, f"step {step}: shares of {n} rows")
+
+
 def test_a_call_makes_its_tensors_on_its_own_stream():
     """No output, no workspace given: the current stream is busy while the side stream's call runs, and
     the memory held other bytes before."""

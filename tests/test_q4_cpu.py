@@ -207,11 +207,11 @@ def test_q4_plans(gd):
     def plan(n_tok, H, Hk, D, n, budget=-1, n_seq=None):
         return gd.plan(n_tok, H, Hk, D, n, budget, gd.KIND_Q4, num_sms=152, n_seq=n_seq)
 
-    # a ragged batch of long rows: one wave of three CTAs an SM with equal shares; counters, then two
-    # records of the group's 4 heads a CTA
+    # a ragged batch of long rows: one wave of three CTAs an SM with equal shares; counters, a
+    # word a row and head, then two records of the group's 4 heads a CTA
     p = plan(16, 32, 8, 128, 32768)
     assert p.streamk == 1 and (p.grid_x, p.grid_y, p.grid_z) == (456, 1, 1)
-    assert p.ws_bytes == 512 + 2 * 456 * 4 * 130 * 4
+    assert p.ws_bytes == 16 * 32 * 4 + 2 * 456 * 4 * 130 * 4
     # short lists, or more rows than the shares are found for: chunks of 2048 positions
     p = plan(200, 32, 8, 128, 1024)
     assert p.streamk == 0 and p.merge == 0 and (p.grid_x, p.grid_y, p.grid_z) == (1, 8, 200)
