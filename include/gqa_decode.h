@@ -147,8 +147,11 @@ size_t attn_decode_workspace_bytes(int n_tok, int n_seq, int n_heads, int n_kv_h
  *                 ceil(n_tok * grid_y * 4 / 256) * 256 bytes are arrival counters (per row,
  *                 or per row group, and KV head): they must be zero before the first call that
  *                 uses this ws (zero the buffer once after allocating it); every call leaves
- *                 them zero again, so the same ws serves any later call.  The rest holds the
- *                 split partials (see attn_decode_workspace_bytes); it needs no clearing.
+ *                 them zero again, so the same ws serves any later call whose counters lie
+ *                 within those of the calls before it (as many rows or fewer); for more rows
+ *                 zero it again, since partials lie there.  (attn_decode_q4 and
+ *                 attn_decode_f16_window need no such care.)  The rest holds the split
+ *                 partials (see attn_decode_workspace_bytes); it needs no clearing.
  *                 Calls sharing a ws must not overlap on the GPU.
  *   err_word      device int32 or NULL
  */
