@@ -234,7 +234,8 @@ def test_decode_balanced(H, Hk, D, ctas):
             assert_close(got, oracle.output_gate(ref, gate.reshape(ref.shape)), TOL, "gate")
 
 
-@pytest.mark.parametrize("H,Hk,D", [(8, 2, 128), (4, 4, 64), (32, 2, 64), (12, 2, 256), (7, 1, 128)])
+@pytest.mark.parametrize("H,Hk,D", [(8, 2, 128), (4, 4, 64), (32, 2, 64), (12, 2, 256), (7, 1, 128),
+                                     (18, 2, 64), (22, 2, 128), (13, 1, 256)])
 @pytest.mark.parametrize("window", [None, 100])
 def test_decode_rows_sharing_sequences(H, Hk, D, window):
     """Causal rows of three sequences in runs, rows out of order, one sequence named twice."""
