@@ -2,14 +2,14 @@
 //
 // A CTA works on a piece of the list of tiles that a (group of rows, KV head x head split) sees: a
 // chunk of it, one a CTA, or, where that would take several waves of long chunks, an equal share of
-// all lists end to end (the 16-row ragged batch: 57.2 us against 69.8).  Each of its four warps
+// all lists end to end (the 16-row ragged batch: 58.0 us against 69.8).  Each of its four warps
 // (eight where a grid leaves no SM a second CTA) streams every fourth (eighth) tile of the piece
 // through a ring of its own and keeps its own running maximum, sum and accumulator, so nothing but
 // the end of the piece synchronises the CTA.  The pieces of a list meet in a cluster of their CTAs'
 // shared memories where one wave of clusters holds the grid, else through the workspace.  A tile
 // is TP positions of one KV head: four contiguous runs of the head-major cache (codes and scales of
-// K and of V), which four lanes copy with cp.async.bulk, one each (the batch 58.0 us, 59.0 where one
-// lane copies all four); the ring holds NST tiles.
+// K and of V), which four lanes copy with cp.async.bulk, one each (one lane copying all four cost the
+// batch another 1.0 us); the ring holds NST tiles.
 //
 // A group is one row, or, where rows share sequences, the consecutive rows whose (row, head) pairs
 // fill the 8 rows of the products that a row's heads leave empty: their tiles are those of the
@@ -33,9 +33,9 @@
 //        interleaved nibble by nibble before the conversion.
 // Rows of 32 or 64 bytes are read without bank conflicts in k.q and two at a time at most in v.p.
 //
-// Bound by instruction issue: 297 warp instructions per 16 positions and KV head (D = 128, 4 heads),
-// 64 conversions and 64 scale products among them, at 64 % of the issue slots; 57 rows of 16384
-// positions take 186 us, 5.8 TB/s, 87 % of the copy rate.
+// Bound by instruction issue: 313 warp instructions per 16 positions and KV head (D = 128, 4 heads),
+// 64 conversions and 64 scale products among them, at 66 % of the issue slots; 57 rows of 16384
+// positions take 188 us, 5.7 TB/s, 86 % of the copy rate.
 #include <atomic>
 #include <type_traits>
 
@@ -84,6 +84,12 @@ struct Q4Cfg {
   static_assert(MIN_CTAS * (SMEM + 2304 + 1024) <= 228 * 1024, "MIN_CTAS fit an SM");
   static_assert(MERGE <= RING && NP * kQ4MaxSplit * 4 <= RING, "merge areas inside the rings");
   static constexpr float RESCALE_LOG2 = 8.f;
+  // Each product of v.p is added to O by fp32 additions, which round; the tensor cores cut the low bits
+  // of what they add to, and that adds up over a long list (16 ragged rows of up to 32768, D = 128:
+  // 1.2e-6 off the 64-bit values and 57.3 us, 4.1e-7 and 58.0 with additions; eight rows of 32768, D =
+  // 64, 64 heads over 8: 1.6e-6 and 57.8 us, 6.2e-7 and 59.1).  Eight pairs of 256 dims have no
+  // registers for it: they would spill (16.5 us for 15.0).
+  static constexpr bool SUMS = D < 256 || PN == 1;
 };
 
 // A run of a group's rows that share a sequence: the union of what they see, as tiles.
@@ -120,6 +126,15 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
+}
+
+// x += y, two sums an instruction.
+__device__ __forceinline__ void add2(float (&x)[4], const float (&y)[4]) {
+  asm("{\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%6, %7};\n\tadd.rn.f32x2 a, a, b;\n\tmov.b64 {%2, %3}, a;\n\t}"
+      : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3])
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]));
 }
 
 // What a CTA works on at a time: tiles [a, b) of a (group z, column y) -- all of its pieces are
@@ -526,8 +541,15 @@ __device__ __forceinline__ void q4_item(const Q4Params& qp, uint8_t* smem, const
               const uint32_t a[4] = {mul_h2(e01[k], s01), mul_h2(o01[k], s01), mul_h2(e23[k], s23),
                                      mul_h2(o23[k], s23)};
 #pragma unroll
-              for (int pn = 0; pn < PN; ++pn)
-                mma_f16(o[pn][4 * ww + k], a, pb[pn][b][0], pb[pn][b][1]);
+              for (int pn = 0; pn < PN; ++pn) {
+                if constexpr (C::SUMS) {
+                  float y[4] = {0.f, 0.f, 0.f, 0.f};
+                  mma_f16(y, a, pb[pn][b][0], pb[pn][b][1]);
+                  add2(o[pn][4 * ww + k], y);
+                } else {
+                  mma_f16(o[pn][4 * ww + k], a, pb[pn][b][0], pb[pn][b][1]);
+                }
+              }
             }
           }
         }

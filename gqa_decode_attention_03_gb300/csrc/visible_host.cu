@@ -18,7 +18,7 @@ bool q4_scale_ok(float s);  // append_q4.cu
 // - A grid that would give every CTA slot kQ4LongShare tiles or more is cut into chunks of kQ4Chunk
 //   positions (64 rows of up to 4096: 52.5 with 1024, 51.7 with 2048), or, where lists are kQ4LongList
 //   positions or longer, into equal shares of all lists in one wave (16 ragged rows of up to 32768:
-//   69.8 chunked, 57.2; 64 of up to 8192 85.5, 76.1; 64 of up to 4096 51.2, 46.0; 200 of up to 1024
+//   69.8 chunked, 58.0; 64 of up to 8192 85.5, 76.1; 64 of up to 4096 51.2, 46.0; 200 of up to 1024
 //   40.9, 49.4).
 // - A smaller one that has an SM for every list runs one CTA of eight warps an SM, a list in as many
 //   chunks as there are SMs (one row of 48 heads over 4, 8191 positions: 14.9 against 18.4 with four
