@@ -128,15 +128,6 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   return r;
 }
 
-// x += y, two sums an instruction.
-__device__ __forceinline__ void add2(float (&x)[4], const float (&y)[4]) {
-  asm("{\n\t.reg .b64 a, b;\n\t"
-      "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%6, %7};\n\tadd.rn.f32x2 a, a, b;\n\tmov.b64 {%2, %3}, a;\n\t}"
-      : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3])
-      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]));
-}
-
 // What a CTA works on at a time: tiles [a, b) of a (group z, column y) -- all of its pieces are
 // merged by the CTA that finishes last.
 struct Q4Item {

@@ -25,9 +25,8 @@ bool q4_scale_ok(float s);  // append_q4.cu
 //   warps; 32 rows of two sequences, window 2048: 13.1 against 17.5).
 constexpr int kQ4Chunk = 2048, kQ4LongShare = 32, kQ4LongList = 2048;
 // Windowed f16 rows: as many chunks as fill the CTA slots once, of at most kWinMaxChunk positions, half
-// as many at D = 256, where a warp sees twice as many of them and its accumulator loses low bits at
-// every product (window 8000, 32 rows of 20 heads over 4: 2.4e-6 off the 64-bit values in chunks of
-// 4000, 185.6 us; 1.7e-6 in chunks of 2048, 168.2 us).
+// as many at D = 256 (window 8000, 32 rows of 20 heads over 4: 185.6 us in chunks of 4000, 168.2 in
+// chunks of 2048).
 constexpr int kWinCtasPerSm = 2;
 constexpr int kWinMaxChunk = 4096, kWinMinStages = 2;
 // Rows sharing a sequence: pairs of a sequence and (4-bit) products of rows, heads and positions from
